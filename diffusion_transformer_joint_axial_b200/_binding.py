@@ -7,6 +7,7 @@ CUDA device is present, every call raises ``QI21Error``: there is no fallback.
 
 import ctypes
 import os
+from collections import namedtuple
 
 import torch
 
@@ -34,6 +35,8 @@ EXPORTED = (
     "qi21_rope_table_size", "qi21_rope_table", "qi21_attn_cached_tabled",
     # projections and the rest of a block of the denoising loop
     "qi21_linear", "qi21_linear_residual", "qi21_linear_swiglu", "qi21_rmsnorm", "qi21_swiglu",
+    # block-scaled 8-bit (MX) forms
+    "qi21_mx_scale_size", "qi21_mx_quantize", "qi21_rmsnorm_mx", "qi21_linear_mx", "qi21_linear_swiglu_mx",
     # status, errors, counters, timing and self-tests
     "qi21_workspace_status", "qi21_status_string", "qi21_last_error", "qi21_launch_count",
     "qi21_selftest_wait_timeout",
@@ -92,6 +95,17 @@ def load_library(path=LIB_PATH):
     L.qi21_rmsnorm.restype = _i32
     L.qi21_swiglu.argtypes = [_i64, _vp, _vp, _vp, _vp]
     L.qi21_swiglu.restype = _i32
+    L.qi21_mx_scale_size.argtypes = [_i64, _i64]
+    L.qi21_mx_scale_size.restype = _sz
+    L.qi21_mx_quantize.argtypes = [_i64, _i64, _vp, _vp, _vp, _vp]
+    L.qi21_mx_quantize.restype = _i32
+    L.qi21_rmsnorm_mx.argtypes = [_i64, _i32, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _vp]
+    L.qi21_rmsnorm_mx.restype = _i32
+    L.qi21_linear_mx.argtypes = [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _vp, ctypes.c_float,
+                                 ctypes.POINTER(_vp), _i32, _vp, _sz, _vp]
+    L.qi21_linear_mx.restype = _i32
+    L.qi21_linear_swiglu_mx.argtypes = [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+    L.qi21_linear_swiglu_mx.restype = _i32
     L.qi21_workspace_status.argtypes = [_vp, _vp]
     L.qi21_selftest_wait_timeout.argtypes = [_vp, _i64, _vp]
     L.qi21_status_string.argtypes = [_i32]
@@ -463,6 +477,156 @@ def swiglu(g, u, out=None):
     _need(out, "out", tuple(g.shape), torch.bfloat16, dev)
     with torch.cuda.device(dev):
         _check(L_.qi21_swiglu(g.numel(), _ptr(g), _ptr(u), _ptr(out), _stream(dev)))
+    return out
+
+
+MXTensor = namedtuple("MXTensor", ("q", "scale"))
+MXTensor.__doc__ = """A block-scaled 8-bit (MX) matrix: ``q`` [..., K] float8_e4m3fn and one power of two
+(float8_e8m0fnu) per 32 consecutive values of a row, ``scale`` [ceil(R / 128), ceil(K / 128), 32, 4, 4]
+with R the product of the leading dimensions: the scale of row r and block b is
+``scale[r // 128, b // 4, r % 32, r % 128 // 32, b % 4]``."""
+
+MX_ACTIVATIONS = {"none": 0, "silu": 1, "gelu_tanh": 2, "gelu": 2}
+
+
+def _rows(shape):
+    n = 1
+    for d in shape[:-1]:
+        n *= d
+    return n
+
+
+def mx_empty(shape, device="cuda"):
+    """An MX matrix to be written: values unset, scale bytes zero (writers leave those of the rows
+    that pad the last group of 128 alone)."""
+    shape = tuple(int(d) for d in shape)
+    R, K = _rows(shape), shape[-1]
+    if K < 32 or K % 32:
+        raise QI21Error(QI21_ERR_INVALID_ARG, "the last dimension must be a multiple of 32 (got %d)" % K)
+    return MXTensor(torch.empty(shape, dtype=torch.float8_e4m3fn, device=device),
+                    torch.zeros(((R + 127) // 128, (K + 127) // 128, 32, 4, 4), dtype=torch.uint8,
+                                device=device).view(torch.float8_e8m0fnu))
+
+
+def _need_mx(t, name, shape, device):
+    if not isinstance(t, MXTensor):
+        raise QI21Error(QI21_ERR_INVALID_ARG, "%s must be an MXTensor" % name)
+    K = shape[-1]
+    _need(t.q, name + ".q", shape, torch.float8_e4m3fn, device)
+    _need(t.scale, name + ".scale", ((_rows(shape) + 127) // 128, (K + 127) // 128, 32, 4, 4),
+          torch.float8_e8m0fnu, device)
+
+
+def _mx_operand(t, name):
+    if not isinstance(t, MXTensor) or not isinstance(t.q, torch.Tensor):
+        raise QI21Error(QI21_ERR_INVALID_ARG, "%s must be an MXTensor" % name)
+    return t.q
+
+
+def mx_quantize(x, out=None):
+    """x (bf16 [..., K], K a multiple of 32) in MX form: weights once, activations such as the
+    attention output in front of a projection."""
+    L_ = _cuda_lib()
+    dev = x.device
+    _need(x, "x", x.shape, torch.bfloat16, dev)
+    if out is None:
+        out = mx_empty(x.shape, dev)
+    _need_mx(out, "out", x.shape, dev)
+    with torch.cuda.device(dev):
+        _check(L_.qi21_mx_quantize(_rows(x.shape), x.shape[-1], x.data_ptr(), out.q.data_ptr(),
+                                   out.scale.data_ptr(), _stream(dev)))
+    return out
+
+
+def rmsnorm_mx(x, w, eps, delta=None, sum_out=None, out=None):
+    """Row RMSNorm of x (bf16 [..., D]) in MX form.  With ``delta`` the residual's addition comes
+    first: h = x + delta is rounded to bf16 and stored (``sum_out``, by default a new tensor; it may be x or
+    delta), the norm is that of the stored h, and the result is ``(h, mx)``; without, just ``mx``."""
+    L_ = _cuda_lib()
+    dev, shape = x.device, x.shape
+    D = shape[-1]
+    _need(x, "x", shape, torch.bfloat16, dev)
+    _need(w, "w", (D,), torch.bfloat16, dev)
+    if delta is not None:
+        _need(delta, "delta", shape, torch.bfloat16, dev)
+        if sum_out is None:
+            sum_out = torch.empty_like(x)
+        _need(sum_out, "sum_out", shape, torch.bfloat16, dev)
+    elif sum_out is not None:
+        raise QI21Error(QI21_ERR_INVALID_ARG, "sum_out is given without delta")
+    if out is None:
+        out = mx_empty(shape, dev)
+    _need_mx(out, "out", shape, dev)
+    with torch.cuda.device(dev):
+        _check(L_.qi21_rmsnorm_mx(_rows(shape), D, x.data_ptr(), delta.data_ptr() if delta is not None else None,
+                                  w.data_ptr(), float(eps), sum_out.data_ptr() if delta is not None else None,
+                                  out.q.data_ptr(), out.scale.data_ptr(), _stream(dev)))
+    return out if delta is None else (sum_out, out)
+
+
+def linear_mx(x, w, bias=None, n_out=1, act="none", residual=None, alpha=1.0, out=None, workspace=None):
+    """alpha * act(X W^T + b) (+ residual) from MX operands, bf16 with fp32 accumulation.
+
+    x: MX [..., K], w: MX [N, K], bias: bf16 [N] or None; act "none", "silu" or "gelu_tanh" (alias
+    "gelu").  As :func:`linear`, the N columns are cut into ``n_out`` segments and the list of ``n_out`` tensors
+    [..., N / n_out] is returned (or ``out``, such a list, filled).  ``residual`` (bf16 [..., N], with
+    n_out = 1) may be ``out[0]``."""
+    L_ = _cuda_lib()
+    xq, wq = _mx_operand(x, "x"), _mx_operand(w, "w")
+    dev, lead, K, N = xq.device, xq.shape[:-1], xq.shape[-1], wq.shape[0]
+    _need_mx(x, "x", xq.shape, dev)
+    _need_mx(w, "w", (N, K), dev)
+    if bias is not None:
+        _need(bias, "bias", (N,), torch.bfloat16, dev)
+    if act not in MX_ACTIVATIONS:
+        raise QI21Error(QI21_ERR_INVALID_ARG, "unknown activation %r" % (act,))
+    if n_out < 1 or N % n_out != 0:
+        raise QI21Error(QI21_ERR_INVALID_ARG, "N=%d does not split into %d segments" % (N, n_out))
+    if residual is not None:
+        _need(residual, "residual", lead + (N,), torch.bfloat16, dev)
+    seg = lead + (N // n_out,)
+    if out is None:
+        out = [torch.empty(seg, dtype=torch.bfloat16, device=dev) for _ in range(n_out)]
+    if len(out) != n_out:
+        raise QI21Error(QI21_ERR_INVALID_ARG, "need %d output tensors" % n_out)
+    for i, o in enumerate(out):
+        _need(o, "out[%d]" % i, seg, torch.bfloat16, dev)
+    if workspace is None:
+        workspace = new_workspace(WORKSPACE_HEADER_BYTES, dev)
+    ptrs = (_vp * n_out)(*[o.data_ptr() for o in out])
+    with torch.cuda.device(dev):
+        _check(L_.qi21_linear_mx(_rows(xq.shape), N, K, xq.data_ptr(), x.scale.data_ptr(), wq.data_ptr(),
+                                 w.scale.data_ptr(), bias.data_ptr() if bias is not None else None,
+                                 MX_ACTIVATIONS[act], residual.data_ptr() if residual is not None else None,
+                                 float(alpha), ptrs, n_out, workspace.data_ptr(),
+                                 workspace.numel() * workspace.element_size(), _stream(dev)))
+    return out
+
+
+def linear_swiglu_mx(x, w_il, bias_il=None, out=None, workspace=None):
+    """silu(X W_gate^T + b_gate) * (X W_up^T + b_up) from MX operands, in MX form: what the down
+    projection reads.  ``w_il`` MX [2F, K] and ``bias_il`` bf16 [2F] in the layout of
+    :func:`interleave_gate_up` (interleave, then :func:`mx_quantize`); returns MX [..., F]."""
+    L_ = _cuda_lib()
+    xq, wq = _mx_operand(x, "x"), _mx_operand(w_il, "w")
+    dev, lead, K, N = xq.device, xq.shape[:-1], xq.shape[-1], wq.shape[0]
+    _need_mx(x, "x", xq.shape, dev)
+    _need_mx(w_il, "w", (N, K), dev)
+    if N % 256:
+        raise QI21Error(QI21_ERR_INVALID_ARG, "the gate and up rows must come in blocks of 128 (N=%d)" % N)
+    if bias_il is not None:
+        _need(bias_il, "bias", (N,), torch.bfloat16, dev)
+    if out is None:
+        out = mx_empty(lead + (N // 2,), dev)
+    _need_mx(out, "out", lead + (N // 2,), dev)
+    if workspace is None:
+        workspace = new_workspace(WORKSPACE_HEADER_BYTES, dev)
+    with torch.cuda.device(dev):
+        _check(L_.qi21_linear_swiglu_mx(_rows(xq.shape), N, K, xq.data_ptr(), x.scale.data_ptr(), wq.data_ptr(),
+                                        w_il.scale.data_ptr(),
+                                        bias_il.data_ptr() if bias_il is not None else None, out.q.data_ptr(),
+                                        out.scale.data_ptr(), workspace.data_ptr(),
+                                        workspace.numel() * workspace.element_size(), _stream(dev)))
     return out
 
 

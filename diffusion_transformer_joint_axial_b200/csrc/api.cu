@@ -603,6 +603,132 @@ qi21_status qi21_swiglu(int64_t n, const void* g, const void* u, void* m, void* 
   return QI21_OK;
 }
 
+size_t qi21_mx_scale_size(int64_t rows, int64_t K) {
+  if (rows < 0 || K < 0) return 0;
+  return (size_t)((rows + 127) / 128) * (size_t)((K + 127) / 128) * 512;
+}
+
+// Sizes and buffers of an MX matrix.
+static qi21_status check_mx_dims(int64_t rows, int64_t K, const char* name) {
+  if (rows < 0 || K < 32 || K % 32 != 0 || rows > INT32_MAX || K > INT32_MAX - 127)
+    return fail(QI21_ERR_INVALID_ARG, "%s: rows must be >= 0 and the length a multiple of 32, >= 32 (got %lld x %lld)",
+                name, (long long)rows, (long long)K);
+  return QI21_OK;
+}
+
+qi21_status qi21_mx_quantize(int64_t M, int64_t K, const void* x, void* q, void* scale, void* stream) {
+  QI21_TRY(check_mx_dims(M, K, "x"));
+  if (M == 0) return QI21_OK;
+  QI21_TRY(check_ptr(x, "x"));
+  QI21_TRY(check_ptr(q, "q"));
+  QI21_TRY(check_ptr(scale, "scale"));
+  cudaError_t e = launch_mx_quantize(M, K, x, q, scale, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "MX quantise launch");
+  return QI21_OK;
+}
+
+qi21_status qi21_rmsnorm_mx(int64_t M, int32_t D, const void* x, const void* delta, const void* w, float eps,
+                            void* sum, void* q, void* scale, void* stream) {
+  QI21_TRY(check_mx_dims(M, D, "x"));
+  if (!(eps >= 0.f) || !(eps < 3.0e38f)) return fail(QI21_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if ((delta == nullptr) != (sum == nullptr))
+    return fail(QI21_ERR_INVALID_ARG, "give both delta and sum or neither");
+  if (M == 0) return QI21_OK;
+  QI21_TRY(check_ptr(x, "x"));
+  if (delta != nullptr) {
+    QI21_TRY(check_ptr(delta, "delta"));
+    QI21_TRY(check_ptr(sum, "sum"));
+  }
+  QI21_TRY(check_ptr(w, "w"));
+  QI21_TRY(check_ptr(q, "q"));
+  QI21_TRY(check_ptr(scale, "scale"));
+  cudaError_t e = launch_rmsnorm_mx(M, D, x, delta, w, eps, sum, q, scale, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "MX RMSNorm launch");
+  return QI21_OK;
+}
+
+// What the two MX products share: sizes, operands, workspace.  *empty: nothing to do.
+static qi21_status mx_gemm_args(MxGemmArgs& a, bool* empty, int64_t M, int64_t N, int64_t K, const void* x,
+                                const void* x_scale, const void* w, const void* w_scale, const void* bias,
+                                void* workspace, size_t workspace_bytes) {
+  QI21_TRY(check_mx_dims(M, K, "x"));
+  QI21_TRY(check_mx_dims(N, K, "w"));
+  *empty = M == 0 || N == 0;
+  if (*empty) return QI21_OK;
+  QI21_TRY(check_ptr(x, "x"));
+  QI21_TRY(check_ptr(x_scale, "x_scale"));
+  QI21_TRY(check_ptr(w, "w"));
+  QI21_TRY(check_ptr(w_scale, "w_scale"));
+  if (bias != nullptr) QI21_TRY(check_ptr(bias, "bias"));
+  QI21_TRY(check_ptr(workspace, "workspace"));
+  if (workspace_bytes < QI21_WORKSPACE_HEADER_BYTES)
+    return fail(QI21_ERR_INVALID_ARG, "workspace too small: %zu < %d bytes", workspace_bytes,
+                QI21_WORKSPACE_HEADER_BYTES);
+  memset(&a, 0, sizeof(a));
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.x = x;
+  a.x_scale = x_scale;
+  a.w = w;
+  a.w_scale = w_scale;
+  a.bias = bias;
+  a.alpha = 1.0f;
+  a.n_out = 1;
+  a.status = static_cast<uint32_t*>(workspace);
+  return QI21_OK;
+}
+
+qi21_status qi21_linear_mx(int64_t M, int64_t N, int64_t K, const void* x, const void* x_scale, const void* w,
+                           const void* w_scale, const void* bias, int32_t act, const void* residual, float alpha,
+                           void* const* out, int32_t n_out, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  if (n_out < 1 || n_out > 4) return fail(QI21_ERR_INVALID_ARG, "n_out must be in [1, 4] (got %d)", n_out);
+  if (N % n_out != 0 || (N / n_out) % 8 != 0)
+    return fail(QI21_ERR_INVALID_ARG, "N / n_out must be a whole multiple of 8 (N=%lld, n_out=%d)", (long long)N,
+                n_out);
+  if (act < QI21_ACT_NONE || act > QI21_ACT_GELU_TANH)
+    return fail(QI21_ERR_INVALID_ARG, "unknown activation %d", act);
+  if (residual != nullptr && n_out != 1) return fail(QI21_ERR_INVALID_ARG, "a residual needs n_out = 1");
+  if (!(alpha == alpha) || alpha > 3.0e38f || alpha < -3.0e38f)
+    return fail(QI21_ERR_INVALID_ARG, "alpha must be finite");
+  MxGemmArgs a;
+  bool empty;
+  QI21_TRY(mx_gemm_args(a, &empty, M, N, K, x, x_scale, w, w_scale, bias, workspace, workspace_bytes));
+  if (empty) return QI21_OK;
+  if (residual != nullptr) QI21_TRY(check_ptr(residual, "residual"));
+  if (out == nullptr) return fail(QI21_ERR_INVALID_ARG, "out is NULL");
+  for (int i = 0; i < n_out; ++i) QI21_TRY(check_ptr(out[i], "out[i]"));
+  a.act = act;
+  a.residual = residual;
+  a.alpha = alpha;
+  for (int i = 0; i < n_out; ++i) a.out[i] = out[i];
+  a.n_out = n_out;
+  cudaError_t e = launch_mx_gemm(a, static_cast<cudaStream_t>(stream), sm_count());
+  if (e != cudaSuccess) return cuda_fail(e, "MX linear launch");
+  return QI21_OK;
+}
+
+qi21_status qi21_linear_swiglu_mx(int64_t M, int64_t N, int64_t K, const void* x, const void* x_scale,
+                                  const void* w, const void* w_scale, const void* bias, void* q, void* scale,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  if (N % 256 != 0)
+    return fail(QI21_ERR_INVALID_ARG, "N must be a multiple of 256 (gate/up blocks of 128; got %lld)",
+                (long long)N);
+  MxGemmArgs a;
+  bool empty;
+  QI21_TRY(mx_gemm_args(a, &empty, M, N, K, x, x_scale, w, w_scale, bias, workspace, workspace_bytes));
+  if (empty) return QI21_OK;
+  QI21_TRY(check_ptr(q, "q"));
+  QI21_TRY(check_ptr(scale, "scale"));
+  a.gated = 1;
+  a.q = q;
+  a.q_scale = scale;
+  cudaError_t e = launch_mx_gemm(a, static_cast<cudaStream_t>(stream), sm_count());
+  if (e != cudaSuccess) return cuda_fail(e, "MX SwiGLU launch");
+  return QI21_OK;
+}
+
 // NULL names the built-in scratch of qi21_attn_cached_noalloc.
 static qi21_status status_target(void** workspace) {
   if (*workspace != nullptr) return QI21_OK;

@@ -1,0 +1,363 @@
+// Products of MX (8-bit, block-scaled) matrices on the sm_100a tensor cores:
+// out = residual + alpha * act(X W^T + b) in bf16, and the gated half of the
+// feed-forward layer, silu(X Wg^T + bg) * (X Wu^T + bu), in MX form.
+//
+// X is [M, K], W is [N, K], both e4m3 with an e8m0 scale per 32 values along
+// K, so  y[m][n] = sum_b 2^(ex[m][b] + ew[n][b]) * sum_{k in b} x[m][k] w[n][k].
+// tcgen05.mma.kind::mxf8f6f4.block_scale does both sums in fp32: one instruction
+// covers K = 32, one scale block, and takes the scales from tensor memory.
+#include <cudaTypedefs.h>
+#include <string.h>
+
+#include "qi21_internal.h"
+#include "qi21_mx.cuh"
+
+namespace qi21 {
+
+namespace mx {
+
+constexpr int BK = 128;           // one 128-byte swizzle atom of e4m3, four scale blocks
+constexpr int kTileBytes = 512;   // scales of 128 rows x 4 blocks
+constexpr int kMaxOut = 4;
+
+// Instruction descriptor of kind::mxf8f6f4: A and B e4m3 (0), K-major, N >> 3 at
+// bit 17, scales e8m0 (bit 23), M >> 4 at bit 24; which of a scale word's four
+// bytes to use goes to bits 4-5 (B) and 29-30 (A).
+__host__ __device__ constexpr uint32_t idesc(int m, int n) {
+  return ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(m >> 4) << 24);
+}
+__device__ __forceinline__ constexpr uint32_t idesc_block(uint32_t b) { return (b << 4) | (b << 29); }
+
+// Shared-memory descriptor of a K-major operand in 128B-swizzled rows of 128
+// bytes: 8-row groups 1024 B apart, version 1, layout 2.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024u >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// ... and of one scale tile: 32 rows of 16 bytes, 8-row groups 128 B apart, no
+// swizzle.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128u >> 4) << 32) | ((uint64_t)1 << 46);
+}
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, uint32_t bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+
+// One scale tile to tensor memory: row r of 128 goes to lane r % 32 (of every
+// warp's lanes) in column r / 32.
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+// D[tmem] (+)= (A * scales) (B * scales)^T over K = 32.
+__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t sa, uint32_t sb,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(sa), "r"(sb), "r"(accumulate)
+      : "memory");
+}
+
+// y / (1 + exp(-y)); the quotient is exact to a few units of 2^-24, far below
+// the rounding of the output.
+__device__ __forceinline__ float silu(float y) { return __fdividef(y, 1.f + __expf(-y)); }
+// 0.5 y (1 + tanh(u)) = y / (1 + exp(-2u)),  u = sqrt(2/pi) (y + 0.044715 y^3)
+__device__ __forceinline__ float gelu_tanh(float y) {
+  return __fdividef(y, 1.f + __expf(-1.5957691216057308f * fmaf(0.044715f * y * y, y, y)));
+}
+__device__ __forceinline__ float activate(float y, int act) {
+  return act == QI21_ACT_SILU ? silu(y) : act == QI21_ACT_GELU_TANH ? gelu_tanh(y) : y;
+}
+
+struct Params {
+  CUtensorMap tm_x, tm_w, tm_xs, tm_ws;
+  int32_t M, N, K;
+  int32_t n_seg;                  // columns per output segment (swiglu: N / 2)
+  int32_t kt;                     // K steps of 128
+  int32_t act;
+  float alpha;
+  __nv_bfloat16* out[kMaxOut];    // [M, n_seg] each
+  const __nv_bfloat16* bias;      // [N] or null
+  const __nv_bfloat16* residual;  // [M, N] or null (may be out[0])
+  uint8_t* q;                     // swiglu: [M, N / 2] e4m3 and its scale tiles
+  uint8_t* scale;
+  int32_t q_tile_cols;
+  uint32_t* status;
+};
+
+// ----------------------------------------------------------------- one tile
+// A CTA computes 128 features x BN tokens: the features (rows of W) take the
+// 128 lanes of tensor memory, so few tokens waste nothing of the W stream, and
+// a warp's store covers 32 neighbouring features of one token.  The gated form takes a
+// gate block and its up block (NW = 2).
+//   warp 0     TMA producer
+//   warp 1     TMEM owner and MMA issuer
+//   warps 2-5  epilogue: one feature per thread
+template <int BN, bool GATED>
+struct Narrow {
+  static constexpr int NW = GATED ? 2 : 1;
+  static constexpr int kW = 128 * BK, kX = BN * BK;
+  static constexpr int kStageBytes = NW * (kW + kTileBytes) + kX + kTileBytes;
+  static constexpr int kStages = 3;
+  static constexpr int kSlot = 4 * NW + 4;  // scale columns of one K step
+  static constexpr uint32_t kScaleCol = NW * BN;
+  static constexpr uint32_t kTmemCols = NW * BN + 2 * kSlot <= 64 ? 64 : NW * BN + 2 * kSlot <= 128 ? 128
+                                        : NW * BN + 2 * kSlot <= 256 ? 256 : 512;
+  struct __align__(1024) Smem {
+    uint8_t w[kStages][NW][kW];
+    uint8_t x[kStages][kX < 1024 ? 1024 : kX];
+    uint8_t ws[kStages][NW][kTileBytes];
+    uint8_t xs[kStages][kTileBytes];
+    uint64_t full[kStages], empty[kStages], done;
+    uint32_t tmem_base;
+    int abort_flag;
+  };
+};
+
+constexpr int kNarrowThreads = 192;
+
+template <int BN, bool GATED>
+__global__ void __launch_bounds__(kNarrowThreads) mx_gemm_narrow(const __grid_constant__ Params p) {
+  using C = Narrow<BN, GATED>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  typename C::Smem& S = *reinterpret_cast<typename C::Smem*>(smem_raw + (((raw + 1023u) & ~1023u) - raw));
+  const int warp = threadIdx.x >> 5;
+  volatile int* abort_flag = &S.abort_flag;
+  const int f0 = blockIdx.x * (C::NW * 128), m0 = blockIdx.y * BN;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(smem_u32(&S.full[s]), 1);
+      mbar_init(smem_u32(&S.empty[s]), 1);
+    }
+    mbar_init(smem_u32(&S.done), 1);
+    S.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&S.tmem_base), C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+
+  if (warp == 0) {
+    const bool leader = elect_one_sync();
+    bool ok = true;
+    int it = 0;
+    for (; it < p.kt; ++it) {
+      const int st = it % C::kStages;
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.empty[st]), ((it / C::kStages) & 1u) ^ 1u, abort_flag,
+                                             p.status, 0x700 | st));
+      if (!ok) break;
+      if (leader) {
+        const uint32_t bar = smem_u32(&S.full[st]);
+        mbar_arrive_expect_tx(bar, C::kStageBytes);
+#pragma unroll
+        for (int w = 0; w < C::NW; ++w) {
+          tma_load_2d(smem_u32(S.w[st][w]), &p.tm_w, bar, it * BK, f0 + 128 * w);
+          tma_load_3d(smem_u32(S.ws[st][w]), &p.tm_ws, bar, 0, it, (f0 >> 7) + w);
+        }
+        tma_load_2d(smem_u32(S.x[st]), &p.tm_x, bar, it * BK, m0);
+        tma_load_3d(smem_u32(S.xs[st]), &p.tm_xs, bar, 0, it, m0 >> 7);
+      }
+      __syncwarp();
+    }
+    // every load issued lands before the CTA may exit
+    for (int st = 0; !ok && st < C::kStages; ++st)
+      if (it > st) mbar_wait(smem_u32(&S.full[st]), ((it - 1 - st) / C::kStages) & 1u, nullptr, nullptr, 0);
+    __syncwarp();
+  } else if (warp == 1) {
+    const bool leader = elect_one_sync();
+    bool ok = true;
+    for (int it = 0; it < p.kt; ++it) {
+      const int st = it % C::kStages;
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.full[st]), (it / C::kStages) & 1u, abort_flag, p.status,
+                                             0x710 | st));
+      // the scale columns of this step were last read by the MMAs of step it - 2
+      if (ok && it >= 2)
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.empty[(it - 2) % C::kStages]),
+                                               ((it - 2) / C::kStages) & 1u, abort_flag, p.status, 0x720 | st));
+      if (!ok) break;
+      tc_fence_after();
+      if (leader) {
+        const uint32_t sf = tmem + C::kScaleCol + (it & 1) * C::kSlot;
+#pragma unroll
+        for (int w = 0; w < C::NW; ++w) copy_scales(sf + 4 * w, scale_desc(smem_u32(S.ws[st][w])));
+        copy_scales(sf + 4 * C::NW, scale_desc(smem_u32(S.xs[st])));
+        const uint64_t xd = operand_desc(smem_u32(S.x[st]));
+        const int blocks = min(4, (p.K - it * BK) >> 5);  // the blocks past K hold nothing
+        for (int b = 0; b < blocks; ++b)
+#pragma unroll
+          for (int w = 0; w < C::NW; ++w)
+            mma_scaled(tmem + w * BN, operand_desc(smem_u32(S.w[st][w])) + 2 * b, xd + 2 * b,
+                       idesc(128, BN) | idesc_block(b), sf + 4 * w, sf + 4 * C::NW, it > 0 || b > 0);
+        mma_commit(smem_u32(&S.empty[st]));
+      }
+      __syncwarp();
+    }
+    // also after a wait that ran out: every MMA issued completes before TMEM is released
+    if (leader) mma_commit(smem_u32(&S.done));
+    __syncwarp();
+    mbar_wait(smem_u32(&S.done), 0, nullptr, p.status, 0x730);
+    __syncwarp();
+  } else {
+    bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.done), 0, abort_flag, p.status, 0x740));
+    ok = ok && !*abort_flag;
+    tc_fence_after();
+    const int quarter = warp & 3, lane = threadIdx.x & 31;
+    const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16);
+    const int j = quarter * 32 + lane;  // feature in the block == TMEM lane
+    const int f = f0 + j;
+    const int last = min(BN, p.M - m0);
+    if (ok && GATED) {
+      const int m_col = (f0 >> 1) + j;  // feature of the hidden layer
+      float bg = 0.f, bu = 0.f;
+      if (p.bias != nullptr) {
+        bg = __bfloat162float(p.bias[f]);
+        bu = __bfloat162float(p.bias[f + 128]);
+      }
+      for (int t = 0; t < last; t += 16) {
+        uint32_t g[16], u[16];
+        tmem_ld16(base + t, g);
+        tmem_ld16(base + BN + t, u);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          if (t + e >= last) break;
+          const int64_t row = m0 + t + e;
+          const float y = silu(__uint_as_float(g[e]) + bg) * (__uint_as_float(u[e]) + bu);
+          const uint32_t byte = mx_scale_byte(__reduce_max_sync(0xffffffffu, abs_bits(y)));
+          p.q[row * p.n_seg + m_col] = (uint8_t)mx_cvt2(y * mx_inv_scale(byte), 0.f);
+          if (lane == 0) p.scale[mx_scale_word(row, m_col >> 7, p.q_tile_cols) + quarter] = (uint8_t)byte;
+        }
+      }
+    } else if (ok) {
+      const bool live = f < p.N;
+      const int seg = live ? f / p.n_seg : 0;
+      const float b = live && p.bias != nullptr ? __bfloat162float(p.bias[f]) : 0.f;
+      __nv_bfloat16* out = p.out[seg] + (f - seg * p.n_seg);
+      for (int t = 0; t < last; t += 16) {
+        uint32_t v[16];
+        tmem_ld16(base + t, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          if (t + e >= last) break;
+          const int64_t row = m0 + t + e;
+          float y = activate(__uint_as_float(v[e]) + b, p.act);
+          // read and written by the same thread: the residual may be the output
+          if (live && p.residual != nullptr)
+            y = fmaf(p.alpha, y, __bfloat162float(p.residual[row * p.N + f]));
+          else
+            y *= p.alpha;
+          if (live) out[row * p.n_seg] = __float2bfloat16(y);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+}
+
+}  // namespace mx
+
+// --------------------------------------------------------------- host side
+static PFN_cuTensorMapEncodeTiled_v12000 mx_encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e =
+        cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q);
+    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr)
+                                                                : nullptr;
+  }();
+  return fn;
+}
+
+// 2-D map of a row-major [rows, K] e4m3 matrix; box 128 (K) x box_rows, 128-byte
+// swizzle, zero fill past the ends.
+static bool encode_values(CUtensorMap* m, const void* base, uint64_t rows, uint64_t K, uint32_t box_rows) {
+  auto fn = mx_encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {K, rows};
+  cuuint64_t strides[1] = {K};
+  cuuint32_t box[2] = {(cuuint32_t)mx::BK, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 3-D map of the scale tiles of [rows, K]: (512 bytes as 128 words, tile column,
+// row group); a box is `groups` tiles of one tile column.  Row groups past the end
+// read as zero (a finite scale).
+static bool encode_scales(CUtensorMap* m, const void* base, uint64_t rows, uint64_t K, uint32_t groups) {
+  auto fn = mx_encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t cols = (K + 127) / 128;
+  cuuint64_t dims[3] = {128, cols, (rows + 127) / 128};
+  cuuint64_t strides[2] = {mx::kTileBytes, cols * mx::kTileBytes};
+  cuuint32_t box[3] = {128, 1, groups};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BN, bool GATED>
+static cudaError_t launch_narrow(mx::Params& p, const MxGemmArgs& a, cudaStream_t stream) {
+  using C = mx::Narrow<BN, GATED>;
+  if (!encode_values(&p.tm_x, a.x, a.M, a.K, BN) || !encode_values(&p.tm_w, a.w, a.N, a.K, 128) ||
+      !encode_scales(&p.tm_xs, a.x_scale, a.M, a.K, 1) || !encode_scales(&p.tm_ws, a.w_scale, a.N, a.K, 1))
+    return cudaErrorInvalidValue;
+  const size_t smem = sizeof(typename C::Smem) + 1024;
+  cudaError_t err = cudaFuncSetAttribute(mx::mx_gemm_narrow<BN, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)smem);
+  if (err != cudaSuccess) return err;
+  const dim3 grid((unsigned)((a.N + C::NW * 128 - 1) / (C::NW * 128)), (unsigned)((a.M + BN - 1) / BN));
+  mx::mx_gemm_narrow<BN, GATED><<<grid, mx::kNarrowThreads, smem, stream>>>(p);
+  note_launch();
+  return cudaGetLastError();
+}
+
+cudaError_t launch_mx_gemm(const MxGemmArgs& a, cudaStream_t stream, int num_sms) {
+  if (a.M == 0 || a.N == 0) return cudaSuccess;
+  mx::Params p;
+  memset(&p, 0, sizeof(p));
+  p.M = (int32_t)a.M;
+  p.N = (int32_t)a.N;
+  p.K = (int32_t)a.K;
+  p.n_seg = (int32_t)(a.gated ? a.N / 2 : a.N / a.n_out);
+  p.kt = (int32_t)((a.K + mx::BK - 1) / mx::BK);
+  p.act = a.act;
+  p.alpha = a.alpha;
+  for (int i = 0; i < a.n_out; ++i) p.out[i] = static_cast<__nv_bfloat16*>(a.out[i]);
+  p.bias = static_cast<const __nv_bfloat16*>(a.bias);
+  p.residual = static_cast<const __nv_bfloat16*>(a.residual);
+  p.q = static_cast<uint8_t*>(a.q);
+  p.scale = static_cast<uint8_t*>(a.q_scale);
+  p.q_tile_cols = p.n_seg / 128;
+  p.status = a.status;
+  return a.gated ? launch_narrow<128, true>(p, a, stream) : launch_narrow<128, false>(p, a, stream);
+}
+
+}  // namespace qi21

@@ -154,6 +154,27 @@ cudaError_t launch_rmsnorm(int64_t M, int32_t D, const void* x, const void* w, f
 // m = silu(g) * u elementwise (bf16, n a multiple of 8).
 cudaError_t launch_swiglu(int64_t n, const void* g, const void* u, void* m, cudaStream_t stream);
 
+// ------------------------------------------------------- MX (8-bit) forms
+cudaError_t launch_mx_quantize(int64_t M, int64_t K, const void* x, void* q, void* scale, cudaStream_t stream);
+// h = x (+ delta -> sum); MX of h / sqrt(mean(h^2) + eps) * w.
+cudaError_t launch_rmsnorm_mx(int64_t M, int32_t D, const void* x, const void* delta, const void* w, float eps,
+                              void* sum, void* q, void* scale, cudaStream_t stream);
+struct MxGemmArgs {
+  int64_t M, N, K;
+  const void *x, *x_scale;  // MX [M, K]
+  const void *w, *w_scale;  // MX [N, K]
+  const void* bias;         // bf16 [N] or null
+  int32_t act;              // qi21_activation
+  const void* residual;     // bf16 [M, N] or null (n_out = 1)
+  float alpha;
+  void* out[4];             // bf16 [M, N / n_out] each (not gated)
+  int32_t n_out;
+  int32_t gated;            // 1: gate/up rows of W alternate in 128-row blocks; MX [M, N / 2] to q, q_scale
+  void *q, *q_scale;
+  uint32_t* status;         // workspace header status word
+};
+cudaError_t launch_mx_gemm(const MxGemmArgs& a, cudaStream_t stream, int num_sms);
+
 // --------------------------------------------------------------- self test
 cudaError_t launch_wait_selftest(uint32_t* status, uint64_t limit_ns, cudaStream_t stream);
 

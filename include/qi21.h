@@ -326,6 +326,82 @@ qi21_status qi21_rmsnorm(int64_t M, int32_t D, const void* x, const void* w, flo
 qi21_status qi21_swiglu(int64_t n, const void* g, const void* u, void* m, void* stream);
 
 /*
+ * Block-scaled 8-bit (MX) forms of the block's row-wise and projection steps: twice
+ * the tensor rate of bf16 and half the bytes of every weight.
+ *
+ * An MX matrix [R, K] (K a multiple of 32) is two device buffers.  Values: e4m3
+ * bytes, row-major.  Scales: one e8m0 byte (exponent + 127) per 32 consecutive
+ * values of a row, in tiles of 128 rows x 4 blocks of 512 bytes, tile (r / 128,
+ * b / 4) at index (r / 128) * ceil(K / 128) + b / 4, the byte of row r and block b
+ * at (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4 in it: qi21_mx_scale_size()
+ * bytes.  A value stands for e4m3 * 2^(byte - 127).  Both buffers 16-byte aligned.
+ *
+ * Writers (qi21_mx_quantize, qi21_rmsnorm_mx, qi21_linear_swiglu_mx) choose for a
+ * block with largest magnitude A the smallest exponent e >= -127 with A <= 448 * 2^e
+ * and round x * 2^-e to nearest even, so nothing saturates; a zero block has
+ * byte 0.  A block that holds a NaN or an infinity gets byte 255 and NaN codes
+ * (it reads back as NaN, and so does every product with it).  They write the scales
+ * of their M rows (and zero for the blocks past K in those rows' last tile),
+ * never those of rows past M: readers ignore both.
+ */
+size_t qi21_mx_scale_size(int64_t rows, int64_t K);
+
+/* qi21_mx_quantize -- x (device bf16 [M, K]) to MX form: weights once, activations
+ * such as the attention output in front of a projection.  q: device [M, K] bytes,
+ * scale: device, qi21_mx_scale_size(M, K) bytes, written. */
+qi21_status qi21_mx_quantize(int64_t M, int64_t K, const void* x, void* q, void* scale, void* stream);
+
+/*
+ * qi21_rmsnorm_mx -- qi21_rmsnorm with its output in MX form and, optionally, the
+ * residual's addition in front: h = x + delta, rounded to bf16 and stored in sum,
+ * then q, scale = MX of h / sqrt(mean(h^2) + eps) * w of that stored h (h = x
+ * without delta), in fp32 up to the 8-bit rounding.
+ *   x       device bf16 [M, D]; w device bf16 [D]; D a multiple of 32.
+ *   delta   device bf16 [M, D] or NULL.
+ *   sum     device bf16 [M, D], written; given exactly when delta is.  It may be
+ *           x or delta itself (each value is read before it is written).
+ *   eps     finite, >= 0.
+ *   q, scale  as for qi21_mx_quantize with K = D; they overlap no input.
+ */
+qi21_status qi21_rmsnorm_mx(int64_t M, int32_t D, const void* x, const void* delta, const void* w, float eps,
+                            void* sum, void* q, void* scale, void* stream);
+
+typedef enum {
+  QI21_ACT_NONE = 0,
+  QI21_ACT_SILU = 1,     /* y / (1 + exp(-y)) */
+  QI21_ACT_GELU_TANH = 2 /* y / 2 (1 + tanh(sqrt(2 / pi) (y + 0.044715 y^3))) */
+} qi21_activation;
+
+/*
+ * qi21_linear_mx -- out = alpha * act(X W^T + b) (+ residual) with X [M, K] and
+ * W [N, K] in MX form, accumulated in fp32 and rounded once to bf16: the projections
+ * (n_out segments as in qi21_linear), the down projection and the Euler step
+ * (residual, alpha), and the two-layer MLPs of the text and time embeddings (act).
+ * From one row (a time embedding) to every token of a request.
+ *   x, x_scale  MX [M, K]; w, w_scale  MX [N, K]; K a multiple of 32, >= 32.
+ *   bias        device bf16 [N] or NULL.
+ *   act         qi21_activation.
+ *   residual    device bf16 [M, N] or NULL (n_out = 1 with it); may be out[0].
+ *   alpha       finite.
+ *   out, n_out, workspace  as for qi21_linear.
+ */
+qi21_status qi21_linear_mx(int64_t M, int64_t N, int64_t K, const void* x, const void* x_scale, const void* w,
+                           const void* w_scale, const void* bias, int32_t act, const void* residual, float alpha,
+                           void* const* out, int32_t n_out, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * qi21_linear_swiglu_mx -- qi21_linear_swiglu on MX operands with its result in MX
+ * form: q, scale = MX [M, N / 2] of silu(X W_gate^T + b_gate) * (X W_up^T + b_up),
+ * computed in fp32 up to the 8-bit rounding, which is what the down projection
+ * (qi21_linear_mx) reads.  W and bias hold gate and up rows in alternating blocks of
+ * 128; N a multiple of 256.
+ */
+qi21_status qi21_linear_swiglu_mx(int64_t M, int64_t N, int64_t K, const void* x, const void* x_scale,
+                                  const void* w, const void* w_scale, const void* bias, void* q, void* scale,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * qi21_attn_cached_noalloc -- the cached step of qi21_attn_cached for callers
  * that may not allocate device memory (plugin hosts that only hand over a
  * stream and tensors, servers that reserve all memory at start-up, loops where
