@@ -71,6 +71,36 @@ __device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, u
       : "memory");
 }
 
+// The same for a CTA pair.  Loads go to this CTA's shared memory and complete on a
+// barrier of the pair's first CTA (`bar` is a cluster address); copies and
+// products, issued by the first CTA, run in both.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* map, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* map, uint32_t bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void copy_scales_pair(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+__device__ __forceinline__ void mma_scaled_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t sa,
+                                                uint32_t sb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(sa), "r"(sb), "r"(accumulate)
+      : "memory");
+}
+
 // y / (1 + exp(-y)); the quotient is exact to a few units of 2^-24, far below
 // the rounding of the output.
 __device__ __forceinline__ float silu(float y) { return __fdividef(y, 1.f + __expf(-y)); }
@@ -87,6 +117,7 @@ struct Params {
   int32_t M, N, K;
   int32_t n_seg;                  // columns per output segment (swiglu: N / 2)
   int32_t kt;                     // K steps of 128
+  int32_t mt, nt;                 // tiles along M and N (CTA pairs)
   int32_t act;
   float alpha;
   __nv_bfloat16* out[kMaxOut];    // [M, n_seg] each
@@ -278,6 +309,298 @@ __global__ void __launch_bounds__(kNarrowThreads) mx_gemm_narrow(const __grid_co
   if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
 }
 
+// ---------------------------------------------------------------- CTA pairs
+// A pair of CTAs computes 256 tokens x 256 features, each its 128 tokens (TMEM
+// lanes) of all 256 features: tcgen05.mma.cta_group::2 reads each CTA's 128 rows
+// of X and 128 rows of W, so a CTA loads 32 KB for 128 x 256 x 128 products, two thirds of
+// what it would load alone.  Persistent: pair i walks tiles i, i + pairs, ..., M
+// fastest in groups of kGroup tiles so that pairs at work together share W and X in L2.
+//   warp 0     TMA producer of its CTA's operands (6 stages of K = 128)
+//   warp 1     TMEM owner; in the first CTA it issues the scale copies and the MMAs
+//   warps 4-7  epilogue: one token per thread
+// Tensor memory holds two accumulators of 256 columns that overlap in 32, [0, 256)
+// and [224, 480), and the scales in the last 32.  The epilogue drains the shared
+// columns first and then lets the next tile's MMAs start, so only that part of
+// an epilogue is not hidden.
+constexpr int kWideThreads = 256;
+constexpr int kWideStages = 6;
+constexpr int kGroup = 16;
+constexpr int kOperand = 128 * BK;
+constexpr int kWideStageBytes = 2 * kOperand + 3 * kTileBytes;
+constexpr uint32_t kAccShift = 224;
+constexpr uint32_t kWideScaleCol = 480;  // two slots of 4 (X) + 8 (W) columns
+
+struct __align__(1024) WideSmem {
+  uint8_t x[kWideStages][kOperand];
+  uint8_t w[kWideStages][kOperand];
+  uint8_t ws[kWideStages][2 * kTileBytes];
+  uint8_t xs[kWideStages][kTileBytes];
+  uint64_t full[kWideStages], empty[kWideStages];
+  uint64_t acc_full[2], acc_free, drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+__device__ __forceinline__ void tile_of(const Params& p, int t, int& m, int& n) {
+  const int span = kGroup * p.nt, g = t / span, in = t - g * span;
+  const int rows = min(kGroup, p.mt - g * kGroup);
+  n = in / rows;
+  m = g * kGroup + in - n * rows;
+}
+
+// 32 accumulators plus their biases (bias: 16-byte aligned, shared by every thread).
+__device__ __forceinline__ void add_bias(float (&y)[32], const uint32_t (&v)[32], const __nv_bfloat16* bias) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(v[e]);
+  if (bias != nullptr) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const uint4 b = __ldg(reinterpret_cast<const uint4*>(bias) + g);
+      const uint32_t* bw = reinterpret_cast<const uint32_t*>(&b);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = unpack_bf16x2(bw[e]);
+        y[8 * g + 2 * e] += f.x;
+        y[8 * g + 2 * e + 1] += f.y;
+      }
+    }
+  }
+}
+
+template <bool GATED>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
+    mx_gemm_wide(const __grid_constant__ Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  WideSmem& S = *reinterpret_cast<WideSmem*>(smem_raw + (((raw + 1023u) & ~1023u) - raw));
+  const int warp = threadIdx.x >> 5;
+  volatile int* abort_flag = &S.abort_flag;
+  const uint32_t rank = cluster_rank();
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kWideStages; ++s) {
+      mbar_init(smem_u32(&S.full[s]), 1);
+      mbar_init(smem_u32(&S.empty[s]), 1);
+    }
+    mbar_init(smem_u32(&S.acc_full[0]), 1);
+    mbar_init(smem_u32(&S.acc_full[1]), 1);
+    mbar_init(smem_u32(&S.acc_free), 8);  // one arrival per epilogue warp of the pair
+    mbar_init(smem_u32(&S.drain), 1);
+    S.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc_pair(smem_u32(&S.tmem_base), 512);
+  if (warp == 0 && (threadIdx.x & 31) == 0) {
+    tma_prefetch_desc(&p.tm_x);
+    tma_prefetch_desc(&p.tm_w);
+    tma_prefetch_desc(&p.tm_xs);
+    tma_prefetch_desc(&p.tm_ws);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+  const int tiles = p.mt * p.nt, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const bool leader = elect_one_sync();
+    uint32_t it = 0;
+    bool ok = true;
+    for (int t = pair; t < tiles && ok; t += pairs) {
+      int m, n;
+      tile_of(p, t, m, n);
+      const int m0 = m * 256 + (int)rank * 128, n0 = n * 256 + (int)rank * 128;
+      for (int kb = 0; kb < p.kt; ++kb, ++it) {
+        const int st = it % kWideStages;
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.empty[st]), ((it / kWideStages) & 1u) ^ 1u, abort_flag,
+                                               p.status, 0x800 | st));
+        if (!ok) break;
+        if (leader) {
+          // both CTAs' bytes count on the first CTA's barrier
+          if (rank == 0) mbar_arrive_expect_tx(smem_u32(&S.full[st]), 2 * kWideStageBytes);
+          const uint32_t bar = cluster_addr(smem_u32(&S.full[st]), 0);
+          tma_load_2d_pair(smem_u32(S.x[st]), &p.tm_x, bar, kb * BK, m0);
+          tma_load_2d_pair(smem_u32(S.w[st]), &p.tm_w, bar, kb * BK, n0);
+          tma_load_3d_pair(smem_u32(S.xs[st]), &p.tm_xs, bar, 0, kb, m * 2 + (int)rank);
+          tma_load_3d_pair(smem_u32(S.ws[st]), &p.tm_ws, bar, 0, kb, n * 2);
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok) {
+      // Loads issued must land before the CTAs may exit.  Only the first CTA's
+      // barriers see them; give the second one's the time that they need at most.
+      if (rank == 0) {
+        for (uint32_t st = 0; st < kWideStages; ++st)
+          if (it > st) mbar_wait(smem_u32(&S.full[st]), ((it - 1 - st) / kWideStages) & 1u, nullptr, nullptr, 0);
+      } else {
+        const uint64_t t0 = global_ns();
+        while (global_ns() - t0 < 2000000ull) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1 && rank == 0) {
+    // ---------------------------------------------------------------- MMA
+    const bool leader = elect_one_sync();
+    uint32_t it = 0, tc = 0;
+    bool ok = true;
+    for (int t = pair; t < tiles && ok; t += pairs, ++tc) {
+      if (tc > 0) {  // the columns that this accumulator shares with the last one are drained
+        ok = __all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&S.acc_free), (tc - 1) & 1u, abort_flag, p.status,
+                                                       0x810));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const uint32_t acc = tmem + kAccShift * (tc & 1u);
+      for (int kb = 0; kb < p.kt; ++kb, ++it) {
+        const int st = it % kWideStages;
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.full[st]), (it / kWideStages) & 1u, abort_flag, p.status,
+                                               0x820 | st));
+        // the scale columns of this step were last read by the MMAs of step it - 2
+        if (ok && it >= 2)
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.empty[(it - 2) % kWideStages]),
+                                                 ((it - 2) / kWideStages) & 1u, abort_flag, p.status, 0x830 | st));
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          const uint32_t sx = tmem + kWideScaleCol + (it & 1u) * 12, sw = sx + 4;
+          const uint64_t wsd = scale_desc(smem_u32(S.ws[st]));
+          copy_scales_pair(sx, scale_desc(smem_u32(S.xs[st])));
+          copy_scales_pair(sw, wsd);
+          copy_scales_pair(sw + 4, wsd + (kTileBytes >> 4));
+          const uint64_t xd = operand_desc(smem_u32(S.x[st])), wd = operand_desc(smem_u32(S.w[st]));
+          const int blocks = min(4, (p.K - kb * BK) >> 5);  // the blocks past K hold nothing
+          for (int b = 0; b < blocks; ++b)
+            mma_scaled_pair(acc, xd + 2 * b, wd + 2 * b, idesc(256, 256) | idesc_block(b), sx, sw, kb > 0 || b > 0);
+          mma_commit_pair(smem_u32(&S.empty[st]));
+          if (kb == p.kt - 1) mma_commit_pair(smem_u32(&S.acc_full[tc & 1u]));
+        }
+        __syncwarp();
+      }
+    }
+    // every MMA issued completes before TMEM is released
+    if (leader) mma_commit_pair(smem_u32(&S.drain));
+    __syncwarp();
+    mbar_wait(smem_u32(&S.drain), 0, nullptr, nullptr, 0);
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ----------------------------------------------------------- epilogue
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t free_bar = cluster_addr(smem_u32(&S.acc_free), 0);
+    uint32_t tc = 0;
+    bool ok = true;
+    for (int t = pair; t < tiles && ok; t += pairs, ++tc) {
+      const uint32_t buf = tc & 1u;
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.acc_full[buf]), (tc >> 1) & 1u, abort_flag, p.status,
+                                             0x840 | buf));
+      if (!ok) break;
+      tc_fence_after();
+      int m, n;
+      tile_of(p, t, m, n);
+      const int64_t row = (int64_t)m * 256 + rank * 128 + (threadIdx.x - 128);
+      const int n0 = n * 256;
+      const bool live = row < p.M;
+      const uint32_t acc = lane_base + kAccShift * buf;
+      // the shared columns, first drained: the last of buffer 0, the first of buffer 1
+      constexpr int kChunks = GATED ? 4 : 8;
+      uint32_t word = 0;  // the row's four scale bytes
+#pragma unroll 1
+      for (int i = 0; i < kChunks; ++i) {
+        const int c = buf == 0 ? (i == 0 ? kChunks - 1 : i - 1) * 32 : i * 32;
+        uint32_t v[32], u[32];
+        tmem_ld32(acc + c, v);
+        if (GATED) tmem_ld32(acc + 128 + c, u);
+        tmem_wait_ld();
+        if (i == 0) {
+          tc_fence_before();
+          __syncwarp();
+          if ((threadIdx.x & 31) == 0) mbar_arrive_cluster(free_bar);
+        }
+        float y[32];
+        if (GATED) {
+          float up[32];
+          add_bias(y, v, p.bias != nullptr ? p.bias + n0 + c : nullptr);
+          add_bias(up, u, p.bias != nullptr ? p.bias + n0 + 128 + c : nullptr);
+          uint32_t top = 0;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            y[e] = silu(y[e]) * up[e];
+            top = max(top, abs_bits(y[e]));
+          }
+          const uint32_t byte = mx_scale_byte(top);
+          const float inv = mx_inv_scale(byte);
+          word |= byte << (c >> 2);
+          if (live) {
+            uint4* q = reinterpret_cast<uint4*>(p.q + row * p.n_seg + (n0 >> 1) + c);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              uint4 o;
+              o.x = mx_cvt4(y[16 * g] * inv, y[16 * g + 1] * inv, y[16 * g + 2] * inv, y[16 * g + 3] * inv);
+              o.y = mx_cvt4(y[16 * g + 4] * inv, y[16 * g + 5] * inv, y[16 * g + 6] * inv, y[16 * g + 7] * inv);
+              o.z = mx_cvt4(y[16 * g + 8] * inv, y[16 * g + 9] * inv, y[16 * g + 10] * inv, y[16 * g + 11] * inv);
+              o.w = mx_cvt4(y[16 * g + 12] * inv, y[16 * g + 13] * inv, y[16 * g + 14] * inv, y[16 * g + 15] * inv);
+              q[g] = o;
+            }
+          }
+        } else if (live) {
+          // bias, output and residual come in 16-byte chunks of 8 columns, N a multiple of 8
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int col = n0 + c + 8 * g;
+            if (col >= p.N) break;
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * g + e]);
+            if (p.bias != nullptr) {
+              const uint4 bb = __ldg(reinterpret_cast<const uint4*>(p.bias + col));
+              const uint32_t* bw = reinterpret_cast<const uint32_t*>(&bb);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 bf = unpack_bf16x2(bw[e]);
+                f[2 * e] += bf.x;
+                f[2 * e + 1] += bf.y;
+              }
+            }
+            if (p.act != QI21_ACT_NONE) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) f[e] = activate(f[e], p.act);
+            }
+            if (p.residual != nullptr) {
+              // read and written by the same thread: the residual may be the output
+              const uint4 rr = *reinterpret_cast<const uint4*>(p.residual + row * p.N + col);
+              const uint32_t* rw = reinterpret_cast<const uint32_t*>(&rr);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 rf = unpack_bf16x2(rw[e]);
+                f[2 * e] = fmaf(p.alpha, f[2 * e], rf.x);
+                f[2 * e + 1] = fmaf(p.alpha, f[2 * e + 1], rf.y);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) f[e] *= p.alpha;
+            }
+            const int seg = col / p.n_seg;
+            __nv_bfloat16* dst = p.out[seg] + row * p.n_seg + (col - seg * p.n_seg);
+            *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                                        pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+          }
+        }
+      }
+      if (GATED && live)
+        *reinterpret_cast<uint32_t*>(p.scale + mx_scale_word(row, n, p.q_tile_cols)) = word;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
 }  // namespace mx
 
 // --------------------------------------------------------------- host side
@@ -339,6 +662,24 @@ static cudaError_t launch_narrow(mx::Params& p, const MxGemmArgs& a, cudaStream_
   return cudaGetLastError();
 }
 
+template <bool GATED>
+static cudaError_t launch_wide(mx::Params& p, const MxGemmArgs& a, cudaStream_t stream, int num_sms) {
+  if (!encode_values(&p.tm_x, a.x, a.M, a.K, 128) || !encode_values(&p.tm_w, a.w, a.N, a.K, 128) ||
+      !encode_scales(&p.tm_xs, a.x_scale, a.M, a.K, 1) || !encode_scales(&p.tm_ws, a.w_scale, a.N, a.K, 2))
+    return cudaErrorInvalidValue;
+  p.mt = (int32_t)((a.M + 255) / 256);
+  p.nt = (int32_t)((a.N + 255) / 256);
+  const size_t smem = sizeof(mx::WideSmem) + 1024;
+  cudaError_t err =
+      cudaFuncSetAttribute(mx::mx_gemm_wide<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (err != cudaSuccess) return err;
+  const int64_t tiles = (int64_t)p.mt * p.nt;
+  const int64_t pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;
+  mx::mx_gemm_wide<GATED><<<(unsigned)(2 * pairs), mx::kWideThreads, smem, stream>>>(p);
+  note_launch();
+  return cudaGetLastError();
+}
+
 cudaError_t launch_mx_gemm(const MxGemmArgs& a, cudaStream_t stream, int num_sms) {
   if (a.M == 0 || a.N == 0) return cudaSuccess;
   mx::Params p;
@@ -357,6 +698,7 @@ cudaError_t launch_mx_gemm(const MxGemmArgs& a, cudaStream_t stream, int num_sms
   p.scale = static_cast<uint8_t*>(a.q_scale);
   p.q_tile_cols = p.n_seg / 128;
   p.status = a.status;
+  if (a.M > 1024) return a.gated ? launch_wide<true>(p, a, stream, num_sms) : launch_wide<false>(p, a, stream, num_sms);
   return a.gated ? launch_narrow<128, true>(p, a, stream) : launch_narrow<128, false>(p, a, stream);
 }
 
