@@ -112,8 +112,10 @@ __device__ __forceinline__ float activate(float y, int act) {
   return act == QI21_ACT_SILU ? silu(y) : act == QI21_ACT_GELU_TANH ? gelu_tanh(y) : y;
 }
 
-struct Params {
+struct __align__(64) Params {
   CUtensorMap tm_x, tm_w, tm_xs, tm_ws;
+  CUtensorMap tm_out[kMaxOut];    // pair kernel: 32-row, 128-byte boxes of out[i], or of q
+  int32_t tma_out;                // 1: tm_out is used
   int32_t M, N, K;
   int32_t n_seg;                  // columns per output segment (swiglu: N / 2)
   int32_t kt;                     // K steps of 128
@@ -318,23 +320,26 @@ __global__ void __launch_bounds__(kNarrowThreads) mx_gemm_narrow(const __grid_co
 //   warp 0     TMA producer of its CTA's operands (6 stages of K = 128)
 //   warp 1     TMEM owner; in the first CTA it issues the scale copies and the MMAs
 //   warps 4-7  epilogue: one token per thread
-// Tensor memory holds two accumulators of 256 columns that overlap in 32, [0, 256)
-// and [224, 480), and the scales in the last 32.  The epilogue drains the shared
-// columns first and then lets the next tile's MMAs start, so only that part of
-// an epilogue is not hidden.
+// Tensor memory holds two accumulators of 256 columns that overlap in 64, [0, 256)
+// and [192, 448), and the scales of five K steps in the last 64.  The epilogue drains the
+// shared columns first and then lets the next tile's MMAs start, so only that
+// part of an epilogue is not hidden.
 constexpr int kWideThreads = 256;
 constexpr int kWideStages = 6;
 constexpr int kGroup = 16;
 constexpr int kOperand = 128 * BK;
 constexpr int kWideStageBytes = 2 * kOperand + 3 * kTileBytes;
-constexpr uint32_t kAccShift = 224;
-constexpr uint32_t kWideScaleCol = 480;  // two slots of 4 (X) + 8 (W) columns
+constexpr uint32_t kAccShift = 192;
+constexpr uint32_t kWideScaleCol = 448;
+constexpr uint32_t kSlots = 5;  // of 4 (X) + 8 (W) scale columns each
 
 struct __align__(1024) WideSmem {
   uint8_t x[kWideStages][kOperand];
   uint8_t w[kWideStages][kOperand];
   uint8_t ws[kWideStages][2 * kTileBytes];
   uint8_t xs[kWideStages][kTileBytes];
+  uint8_t stage[4][32 * 128];        // one 32-row, 128-byte box per epilogue warp
+  __nv_bfloat16 bias[2][256];        // of this tile and the next
   uint64_t full[kWideStages], empty[kWideStages];
   uint64_t acc_full[2], acc_free, drain;
   uint32_t tmem_base;
@@ -348,23 +353,40 @@ __device__ __forceinline__ void tile_of(const Params& p, int t, int& m, int& n) 
   m = g * kGroup + in - n * rows;
 }
 
-// 32 accumulators plus their biases (bias: 16-byte aligned, shared by every thread).
+// 32 accumulators plus their biases (in shared memory, the same for every thread).
 __device__ __forceinline__ void add_bias(float (&y)[32], const uint32_t (&v)[32], const __nv_bfloat16* bias) {
 #pragma unroll
-  for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(v[e]);
-  if (bias != nullptr) {
+  for (int g = 0; g < 4; ++g) {
+    const uint4 b = reinterpret_cast<const uint4*>(bias)[g];
+    const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const uint4 b = __ldg(reinterpret_cast<const uint4*>(bias) + g);
-      const uint32_t* bw = reinterpret_cast<const uint32_t*>(&b);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = unpack_bf16x2(bw[e]);
-        y[8 * g + 2 * e] += f.x;
-        y[8 * g + 2 * e + 1] += f.y;
-      }
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = unpack_bf16x2(bw[e]);
+      y[8 * g + 2 * e] = __uint_as_float(v[8 * g + 2 * e]) + f.x;
+      y[8 * g + 2 * e + 1] = __uint_as_float(v[8 * g + 2 * e + 1]) + f.y;
     }
   }
+}
+
+// 16-byte chunk `j` (0..7) of this lane's row in a 128B-swizzled box.
+__device__ __forceinline__ uint4* box_chunk(uint8_t* box, uint32_t lane, uint32_t j) {
+  return reinterpret_cast<uint4*>(box + lane * 128 + ((j ^ (lane & 7u)) << 4));
+}
+// The box of this warp is written: one lane hands it to the TMA.
+__device__ __forceinline__ void store_box(const CUtensorMap* map, uint8_t* box, int c0, int c1) {
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (elect_one_sync()) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(c0),
+                 "r"(c1), "r"(smem_u32(box))
+                 : "memory");
+    bulk_commit_group();
+  }
+}
+// ... and may be written again once the TMA has read it.
+__device__ __forceinline__ void reuse_box() {
+  if (elect_one_sync()) bulk_wait_read_all();
+  __syncwarp();
 }
 
 template <bool GATED>
@@ -405,19 +427,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    const bool leader = elect_one_sync();
-    uint32_t it = 0;
-    bool ok = true;
-    for (int t = pair; t < tiles && ok; t += pairs) {
-      int m, n;
-      tile_of(p, t, m, n);
-      const int m0 = m * 256 + (int)rank * 128, n0 = n * 256 + (int)rank * 128;
-      for (int kb = 0; kb < p.kt; ++kb, ++it) {
-        const int st = it % kWideStages;
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.empty[st]), ((it / kWideStages) & 1u) ^ 1u, abort_flag,
-                                               p.status, 0x800 | st));
-        if (!ok) break;
-        if (leader) {
+    if (elect_one_sync()) {
+      uint32_t it = 0, st = 0, ph = 1;
+      bool ok = true;
+      for (int t = pair; t < tiles && ok; t += pairs) {
+        int m, n;
+        tile_of(p, t, m, n);
+        const int m0 = m * 256 + (int)rank * 128, n0 = n * 256 + (int)rank * 128;
+        for (int kb = 0; kb < p.kt; ++kb, ++it) {
+          ok = mbar_wait(smem_u32(&S.empty[st]), ph, abort_flag, p.status, 0x800 | st);
+          if (!ok) break;
           // both CTAs' bytes count on the first CTA's barrier
           if (rank == 0) mbar_arrive_expect_tx(smem_u32(&S.full[st]), 2 * kWideStageBytes);
           const uint32_t bar = cluster_addr(smem_u32(&S.full[st]), 0);
@@ -425,105 +444,139 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
           tma_load_2d_pair(smem_u32(S.w[st]), &p.tm_w, bar, kb * BK, n0);
           tma_load_3d_pair(smem_u32(S.xs[st]), &p.tm_xs, bar, 0, kb, m * 2 + (int)rank);
           tma_load_3d_pair(smem_u32(S.ws[st]), &p.tm_ws, bar, 0, kb, n * 2);
+          if (++st == kWideStages) st = 0, ph ^= 1u;
         }
-        __syncwarp();
       }
-    }
-    if (!ok) {
-      // Loads issued must land before the CTAs may exit.  Only the first CTA's
-      // barriers see them; give the second one's the time that they need at most.
-      if (rank == 0) {
-        for (uint32_t st = 0; st < kWideStages; ++st)
-          if (it > st) mbar_wait(smem_u32(&S.full[st]), ((it - 1 - st) / kWideStages) & 1u, nullptr, nullptr, 0);
-      } else {
-        const uint64_t t0 = global_ns();
-        while (global_ns() - t0 < 2000000ull) {
+      if (!ok) {
+        // Loads issued must land before the CTAs may exit.  Only the first CTA's
+        // barriers see them; give the second one's the time that they need at most.
+        if (rank == 0) {
+          for (st = 0; st < kWideStages; ++st)
+            if (it > st) mbar_wait(smem_u32(&S.full[st]), ((it - 1 - st) / kWideStages) & 1u, nullptr, nullptr, 0);
+        } else {
+          const uint64_t t0 = global_ns();
+          while (global_ns() - t0 < 2000000ull) {
+          }
         }
       }
     }
     __syncwarp();
   } else if (warp == 1 && rank == 0) {
     // ---------------------------------------------------------------- MMA
-    const bool leader = elect_one_sync();
-    uint32_t it = 0, tc = 0;
-    bool ok = true;
-    for (int t = pair; t < tiles && ok; t += pairs, ++tc) {
-      if (tc > 0) {  // the columns that this accumulator shares with the last one are drained
-        ok = __all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&S.acc_free), (tc - 1) & 1u, abort_flag, p.status,
-                                                       0x810));
-        if (!ok) break;
-        tc_fence_after();
-      }
-      const uint32_t acc = tmem + kAccShift * (tc & 1u);
-      for (int kb = 0; kb < p.kt; ++kb, ++it) {
-        const int st = it % kWideStages;
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.full[st]), (it / kWideStages) & 1u, abort_flag, p.status,
-                                               0x820 | st));
-        // the scale columns of this step were last read by the MMAs of step it - 2
-        if (ok && it >= 2)
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.empty[(it - 2) % kWideStages]),
-                                                 ((it - 2) / kWideStages) & 1u, abort_flag, p.status, 0x830 | st));
-        if (!ok) break;
-        tc_fence_after();
-        if (leader) {
-          const uint32_t sx = tmem + kWideScaleCol + (it & 1u) * 12, sw = sx + 4;
-          const uint64_t wsd = scale_desc(smem_u32(S.ws[st]));
-          copy_scales_pair(sx, scale_desc(smem_u32(S.xs[st])));
+    // One thread runs the whole loop: a stage's products take about 512 cycles, and
+    // a warp-wide loop (votes, an elected branch per stage) took longer than that.
+    if (elect_one_sync()) {
+      uint32_t it = 0, st = 0, ph = 0, slot = 0, tc = 0;
+      bool ok = true;
+      const uint64_t xd0 = operand_desc(smem_u32(S.x[0])), wd0 = operand_desc(smem_u32(S.w[0]));
+      const uint64_t xsd0 = scale_desc(smem_u32(S.xs[0])), wsd0 = scale_desc(smem_u32(S.ws[0]));
+      for (int t = pair; t < tiles && ok; t += pairs, ++tc) {
+        if (tc > 0) {  // the columns that this accumulator shares with the last one are drained
+          ok = mbar_wait_cluster(smem_u32(&S.acc_free), (tc - 1) & 1u, abort_flag, p.status, 0x810);
+          if (!ok) break;
+        }
+        const uint32_t acc = tmem + kAccShift * (tc & 1u);
+        for (int kb = 0; kb < p.kt; ++kb, ++it) {
+          // the scale columns of this slot were last read by the MMAs of step it - kSlots
+          if (it >= kSlots) {
+            const uint32_t was = it - kSlots;
+            ok = mbar_wait(smem_u32(&S.empty[was % kWideStages]), (was / kWideStages) & 1u, abort_flag, p.status,
+                           0x830 | st);
+          }
+          ok = ok && mbar_wait(smem_u32(&S.full[st]), ph, abort_flag, p.status, 0x820 | st);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sx = tmem + kWideScaleCol + slot * 12, sw = sx + 4;
+          const uint64_t xd = xd0 + st * (kOperand >> 4), wd = wd0 + st * (kOperand >> 4);
+          const uint64_t wsd = wsd0 + st * (2 * kTileBytes >> 4);
+          copy_scales_pair(sx, xsd0 + st * (kTileBytes >> 4));
           copy_scales_pair(sw, wsd);
           copy_scales_pair(sw + 4, wsd + (kTileBytes >> 4));
-          const uint64_t xd = operand_desc(smem_u32(S.x[st])), wd = operand_desc(smem_u32(S.w[st]));
-          const int blocks = min(4, (p.K - kb * BK) >> 5);  // the blocks past K hold nothing
-          for (int b = 0; b < blocks; ++b)
-            mma_scaled_pair(acc, xd + 2 * b, wd + 2 * b, idesc(256, 256) | idesc_block(b), sx, sw, kb > 0 || b > 0);
+          const int blocks = (p.K - kb * BK) >> 5;  // the blocks past K hold nothing
+          if (blocks >= 4) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+              mma_scaled_pair(acc, xd + 2 * b, wd + 2 * b, idesc(256, 256) | idesc_block(b), sx, sw, kb > 0 || b > 0);
+          } else {
+            for (int b = 0; b < blocks; ++b)
+              mma_scaled_pair(acc, xd + 2 * b, wd + 2 * b, idesc(256, 256) | idesc_block(b), sx, sw, kb > 0 || b > 0);
+          }
           mma_commit_pair(smem_u32(&S.empty[st]));
           if (kb == p.kt - 1) mma_commit_pair(smem_u32(&S.acc_full[tc & 1u]));
+          if (++st == kWideStages) st = 0, ph ^= 1u;
+          if (++slot == kSlots) slot = 0;
         }
-        __syncwarp();
       }
+      // every MMA issued completes before TMEM is released
+      mma_commit_pair(smem_u32(&S.drain));
+      mbar_wait(smem_u32(&S.drain), 0, nullptr, nullptr, 0);
     }
-    // every MMA issued completes before TMEM is released
-    if (leader) mma_commit_pair(smem_u32(&S.drain));
-    __syncwarp();
-    mbar_wait(smem_u32(&S.drain), 0, nullptr, nullptr, 0);
     __syncwarp();
   } else if (warp >= 4) {
     // ----------------------------------------------------------- epilogue
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t free_bar = cluster_addr(smem_u32(&S.acc_free), 0);
+    const uint32_t tid = threadIdx.x - 128, lane = threadIdx.x & 31;
+    uint8_t* box = S.stage[warp & 3];
     uint32_t tc = 0;
     bool ok = true;
     for (int t = pair; t < tiles && ok; t += pairs, ++tc) {
       const uint32_t buf = tc & 1u;
+      int m, n;
+      tile_of(p, t, m, n);
+      const int n0 = n * 256, row0 = m * 256 + (int)rank * 128 + (warp & 3) * 32;
+      const int64_t row = row0 + lane;
+      const bool live = row < p.M;
+      uint32_t bias2 = 0;  // two columns each; N is even
+      if (p.bias != nullptr && n0 + 2 * (int)tid < p.N)
+        bias2 = __ldg(reinterpret_cast<const uint32_t*>(p.bias + n0) + tid);
+      reinterpret_cast<uint32_t*>(S.bias[buf])[tid] = bias2;
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.acc_full[buf]), (tc >> 1) & 1u, abort_flag, p.status,
                                              0x840 | buf));
       if (!ok) break;
       tc_fence_after();
-      int m, n;
-      tile_of(p, t, m, n);
-      const int64_t row = (int64_t)m * 256 + rank * 128 + (threadIdx.x - 128);
-      const int n0 = n * 256;
-      const bool live = row < p.M;
       const uint32_t acc = lane_base + kAccShift * buf;
-      // the shared columns, first drained: the last of buffer 0, the first of buffer 1
-      constexpr int kChunks = GATED ? 4 : 8;
+      // The shared columns, the last 64 of buffer 0 and the first 64 of buffer 1, leave tensor memory first.
+      uint32_t held[2][32];
+      const uint32_t shared = buf == 0 ? 192 : 0;
+      tmem_ld32(acc + shared, held[0]);
+      tmem_ld32(acc + shared + 32, held[1]);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(free_bar);
+      named_bar_sync(1, 128);  // the biases are there (and the last tile's are no longer read)
+      if (GATED) reuse_box();
       uint32_t word = 0;  // the row's four scale bytes
-#pragma unroll 1
+      constexpr int kChunks = GATED ? 4 : 8;
+#pragma unroll
       for (int i = 0; i < kChunks; ++i) {
-        const int c = buf == 0 ? (i == 0 ? kChunks - 1 : i - 1) * 32 : i * 32;
+        // chunks in the order that uses the held columns first; gated: a held column is an
+        // up column in buffer 0, a gate column in buffer 1
+        const int c = buf == 0 ? ((i + kChunks - 2) % kChunks) * 32 : i * 32;
         uint32_t v[32], u[32];
-        tmem_ld32(acc + c, v);
-        if (GATED) tmem_ld32(acc + 128 + c, u);
-        tmem_wait_ld();
-        if (i == 0) {
-          tc_fence_before();
-          __syncwarp();
-          if ((threadIdx.x & 31) == 0) mbar_arrive_cluster(free_bar);
+        if (i < 2) {
+          if (GATED) tmem_ld32(acc + (buf == 0 ? c : 128 + c), u);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = held[i][e];
+        } else {
+          tmem_ld32(acc + c, v);
+          if (GATED) tmem_ld32(acc + 128 + c, u);
         }
         float y[32];
         if (GATED) {
+          tmem_wait_ld();
+          if (i < 2 && buf == 0) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const uint32_t x = v[e];
+              v[e] = u[e];
+              u[e] = x;
+            }
+          }
           float up[32];
-          add_bias(y, v, p.bias != nullptr ? p.bias + n0 + c : nullptr);
-          add_bias(up, u, p.bias != nullptr ? p.bias + n0 + 128 + c : nullptr);
+          add_bias(y, v, S.bias[buf] + c);
+          add_bias(up, u, S.bias[buf] + 128 + c);
           uint32_t top = 0;
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
@@ -533,65 +586,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
           const uint32_t byte = mx_scale_byte(top);
           const float inv = mx_inv_scale(byte);
           word |= byte << (c >> 2);
-          if (live) {
-            uint4* q = reinterpret_cast<uint4*>(p.q + row * p.n_seg + (n0 >> 1) + c);
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              uint4 o;
-              o.x = mx_cvt4(y[16 * g] * inv, y[16 * g + 1] * inv, y[16 * g + 2] * inv, y[16 * g + 3] * inv);
-              o.y = mx_cvt4(y[16 * g + 4] * inv, y[16 * g + 5] * inv, y[16 * g + 6] * inv, y[16 * g + 7] * inv);
-              o.z = mx_cvt4(y[16 * g + 8] * inv, y[16 * g + 9] * inv, y[16 * g + 10] * inv, y[16 * g + 11] * inv);
-              o.w = mx_cvt4(y[16 * g + 12] * inv, y[16 * g + 13] * inv, y[16 * g + 14] * inv, y[16 * g + 15] * inv);
-              q[g] = o;
-            }
+          for (int g = 0; g < 2; ++g) {
+            uint4 o;
+            o.x = mx_cvt4(y[16 * g] * inv, y[16 * g + 1] * inv, y[16 * g + 2] * inv, y[16 * g + 3] * inv);
+            o.y = mx_cvt4(y[16 * g + 4] * inv, y[16 * g + 5] * inv, y[16 * g + 6] * inv, y[16 * g + 7] * inv);
+            o.z = mx_cvt4(y[16 * g + 8] * inv, y[16 * g + 9] * inv, y[16 * g + 10] * inv, y[16 * g + 11] * inv);
+            o.w = mx_cvt4(y[16 * g + 12] * inv, y[16 * g + 13] * inv, y[16 * g + 14] * inv, y[16 * g + 15] * inv);
+            *box_chunk(box, lane, (c >> 4) + g) = o;
           }
-        } else if (live) {
-          // bias, output and residual come in 16-byte chunks of 8 columns, N a multiple of 8
+        } else {
+          if (n0 + (c & ~63) >= p.N) continue;  // (both chunks of a box alike)
+          uint4 res[4] = {};
+          if (p.residual != nullptr && live) {
+            const uint4* r = reinterpret_cast<const uint4*>(p.residual + row * p.N + n0 + c);
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              if (n0 + c + 8 * g < p.N) res[g] = r[g];
+          }
+          tmem_wait_ld();
+          add_bias(y, v, S.bias[buf] + c);
+          if (p.act == QI21_ACT_SILU) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) y[e] = silu(y[e]);
+          } else if (p.act == QI21_ACT_GELU_TANH) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) y[e] = gelu_tanh(y[e]);
+          }
+          if ((i & 1) == 0 && p.tma_out) reuse_box();
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const int col = n0 + c + 8 * g;
-            if (col >= p.N) break;
-            float f[8];
+            const uint32_t rw[4] = {res[g].x, res[g].y, res[g].z, res[g].w};
+            uint32_t o[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * g + e]);
-            if (p.bias != nullptr) {
-              const uint4 bb = __ldg(reinterpret_cast<const uint4*>(p.bias + col));
-              const uint32_t* bw = reinterpret_cast<const uint32_t*>(&bb);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 bf = unpack_bf16x2(bw[e]);
-                f[2 * e] += bf.x;
-                f[2 * e + 1] += bf.y;
+            for (int e = 0; e < 4; ++e) {
+              const float2 rf = unpack_bf16x2(rw[e]);
+              float a = y[8 * g + 2 * e] * p.alpha, b = y[8 * g + 2 * e + 1] * p.alpha;
+              if (p.residual != nullptr) {
+                a = fmaf(p.alpha, y[8 * g + 2 * e], rf.x);
+                b = fmaf(p.alpha, y[8 * g + 2 * e + 1], rf.y);
               }
+              o[e] = pack_bf16x2(a, b);
             }
-            if (p.act != QI21_ACT_NONE) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) f[e] = activate(f[e], p.act);
+            const uint4 ov = make_uint4(o[0], o[1], o[2], o[3]);
+            if (p.tma_out) {
+              *box_chunk(box, lane, ((c >> 3) & 7) + g) = ov;
+            } else if (live && n0 + c + 8 * g < p.N) {
+              const int col = n0 + c + 8 * g, seg = col / p.n_seg;
+              *reinterpret_cast<uint4*>(p.out[seg] + row * p.n_seg + (col - seg * p.n_seg)) = ov;
             }
-            if (p.residual != nullptr) {
-              // read and written by the same thread: the residual may be the output
-              const uint4 rr = *reinterpret_cast<const uint4*>(p.residual + row * p.N + col);
-              const uint32_t* rw = reinterpret_cast<const uint32_t*>(&rr);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 rf = unpack_bf16x2(rw[e]);
-                f[2 * e] = fmaf(p.alpha, f[2 * e], rf.x);
-                f[2 * e + 1] = fmaf(p.alpha, f[2 * e + 1], rf.y);
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) f[e] *= p.alpha;
-            }
-            const int seg = col / p.n_seg;
-            __nv_bfloat16* dst = p.out[seg] + row * p.n_seg + (col - seg * p.n_seg);
-            *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                                        pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+          }
+          if ((i & 1) == 1 && p.tma_out) {
+            // 64 columns are done; rows and columns past the end are not written
+            const int col = n0 + (c & ~63), seg = col / p.n_seg;
+            if (row0 < p.M) store_box(&p.tm_out[seg], box, col - seg * p.n_seg, row0);
           }
         }
       }
-      if (GATED && live)
-        *reinterpret_cast<uint32_t*>(p.scale + mx_scale_word(row, n, p.q_tile_cols)) = word;
+      if (GATED) {
+        if (row0 < p.M) store_box(&p.tm_out[0], box, n0 >> 1, row0);
+        if (live) *reinterpret_cast<uint32_t*>(p.scale + mx_scale_word(row, n, p.q_tile_cols)) = word;
+      }
     }
+    reuse_box();  // the TMA has read what it was given
   }
 
   tc_fence_before();
@@ -646,6 +703,20 @@ static bool encode_scales(CUtensorMap* m, const void* base, uint64_t rows, uint6
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 2-D map of a row-major result; boxes of 32 rows x 128 bytes, 128-byte swizzle.
+static bool encode_out(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t bytes) {
+  auto fn = mx_encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {cols * bytes};
+  cuuint32_t box[2] = {128 / bytes, 32};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int BN, bool GATED>
 static cudaError_t launch_narrow(mx::Params& p, const MxGemmArgs& a, cudaStream_t stream) {
   using C = mx::Narrow<BN, GATED>;
@@ -667,6 +738,11 @@ static cudaError_t launch_wide(mx::Params& p, const MxGemmArgs& a, cudaStream_t 
   if (!encode_values(&p.tm_x, a.x, a.M, a.K, 128) || !encode_values(&p.tm_w, a.w, a.N, a.K, 128) ||
       !encode_scales(&p.tm_xs, a.x_scale, a.M, a.K, 1) || !encode_scales(&p.tm_ws, a.w_scale, a.N, a.K, 2))
     return cudaErrorInvalidValue;
+  // The result leaves through 32-row, 128-byte boxes, except where a segment
+  // ends inside of one.
+  p.tma_out = GATED || a.n_out == 1 || p.n_seg % 64 == 0;
+  for (int i = 0; p.tma_out && i < a.n_out; ++i)
+    if (!encode_out(&p.tm_out[i], GATED ? a.q : a.out[i], a.M, p.n_seg, GATED ? 1 : 2)) return cudaErrorInvalidValue;
   p.mt = (int32_t)((a.M + 255) / 256);
   p.nt = (int32_t)((a.N + 255) / 256);
   const size_t smem = sizeof(mx::WideSmem) + 1024;
