@@ -131,49 +131,62 @@ struct __align__(64) Params {
   uint32_t* status;
 };
 
-// ----------------------------------------------------------------- one tile
-// A CTA computes 128 features x BN tokens: the features (rows of W) take the
-// 128 lanes of tensor memory, so few tokens waste nothing of the W stream, and
-// a warp's store covers 32 neighbouring features of one token.  The gated form takes a
-// gate block and its up block (NW = 2).
+// ----------------------------------------------------------- few tokens
+// A CTA computes 128 features x bn tokens (bn a multiple of 16, at most 128): the features
+// (rows of W) take the 128 lanes of tensor memory, so few tokens waste nothing of
+// the stream of W, which is what bounds these calls; a warp's store covers 32
+// neighbouring features of one token.  The gated form takes a gate block and its up
+// block.  With few tiles the K axis is split over a cluster: each CTA leaves its
+// partial sums in its shared memory, and each adds up and finishes a share of
+// the tokens, reading the others' partials in the order of the split.
 //   warp 0     TMA producer
 //   warp 1     TMEM owner and MMA issuer
 //   warps 2-5  epilogue: one feature per thread
-template <int BN, bool GATED>
+//
+// Tensor memory and residency: a CTA waits in its allocation while others of the
+// SM hold the columns, and CTAs of a cluster wait for one another, so an SM must
+// never host CTAs that want more than its 512 columns together.  Shared memory sees to
+// that: at most 256 columns with at least 76 KB (two such CTAs fit), or 512 with more
+// than 151 KB (nothing else fits beside it).
+constexpr int kNarrowThreads = 192;
+constexpr int kNarrowMaxStages = 8;
+constexpr int kNarrowSlots = 4;
+constexpr int kW = 128 * BK;
+
 struct Narrow {
-  static constexpr int NW = GATED ? 2 : 1;
-  static constexpr int kW = 128 * BK, kX = BN * BK;
-  static constexpr int kStageBytes = NW * (kW + kTileBytes) + kX + kTileBytes;
-  static constexpr int kStages = 3;
-  static constexpr int kSlot = 4 * NW + 4;  // scale columns of one K step
-  static constexpr uint32_t kScaleCol = NW * BN;
-  static constexpr uint32_t kTmemCols = NW * BN + 2 * kSlot <= 64 ? 64 : NW * BN + 2 * kSlot <= 128 ? 128
-                                        : NW * BN + 2 * kSlot <= 256 ? 256 : 512;
-  struct __align__(1024) Smem {
-    uint8_t w[kStages][NW][kW];
-    uint8_t x[kStages][kX < 1024 ? 1024 : kX];
-    uint8_t ws[kStages][NW][kTileBytes];
-    uint8_t xs[kStages][kTileBytes];
-    uint64_t full[kStages], empty[kStages], done;
-    uint32_t tmem_base;
-    int abort_flag;
-  };
+  int32_t bn, stages, cols, split, smem;
 };
 
-constexpr int kNarrowThreads = 192;
+struct NarrowBars {
+  uint64_t full[kNarrowMaxStages], empty[kNarrowMaxStages], done;
+  uint32_t tmem_base;
+  int abort_flag;
+};
 
-template <int BN, bool GATED>
-__global__ void __launch_bounds__(kNarrowThreads) mx_gemm_narrow(const __grid_constant__ Params p) {
-  using C = Narrow<BN, GATED>;
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <bool GATED>
+__global__ void __launch_bounds__(kNarrowThreads) mx_gemm_narrow(const __grid_constant__ Params p, const Narrow c) {
+  constexpr int NW = GATED ? 2 : 1;
+  constexpr int kSlot = 4 * NW + 4;  // scale columns of one K step
   extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  typename C::Smem& S = *reinterpret_cast<typename C::Smem*>(smem_raw + (((raw + 1023u) & ~1023u) - raw));
+  __shared__ NarrowBars S;
+  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+  const uint32_t kx = (uint32_t)c.bn * BK;
+  const uint32_t sw = base, sx = sw + c.stages * NW * kW, sws = sx + c.stages * kx,
+                 sxs = sws + c.stages * NW * kTileBytes;
   const int warp = threadIdx.x >> 5;
   volatile int* abort_flag = &S.abort_flag;
-  const int f0 = blockIdx.x * (C::NW * 128), m0 = blockIdx.y * BN;
+  const int rank = c.split > 1 ? (int)cluster_rank() : 0;
+  const int f0 = (int)(blockIdx.x / c.split) * (NW * 128), m0 = blockIdx.y * c.bn;
+  const int k_begin = (int)((int64_t)p.kt * rank / c.split), k_end = (int)((int64_t)p.kt * (rank + 1) / c.split);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
+    for (int s = 0; s < c.stages; ++s) {
       mbar_init(smem_u32(&S.full[s]), 1);
       mbar_init(smem_u32(&S.empty[s]), 1);
     }
@@ -182,7 +195,7 @@ __global__ void __launch_bounds__(kNarrowThreads) mx_gemm_narrow(const __grid_co
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&S.tmem_base), C::kTmemCols);
+    tmem_alloc(smem_u32(&S.tmem_base), c.cols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -191,124 +204,157 @@ __global__ void __launch_bounds__(kNarrowThreads) mx_gemm_narrow(const __grid_co
   const uint32_t tmem = S.tmem_base;
 
   if (warp == 0) {
-    const bool leader = elect_one_sync();
-    bool ok = true;
-    int it = 0;
-    for (; it < p.kt; ++it) {
-      const int st = it % C::kStages;
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.empty[st]), ((it / C::kStages) & 1u) ^ 1u, abort_flag,
-                                             p.status, 0x700 | st));
-      if (!ok) break;
-      if (leader) {
+    if (elect_one_sync()) {
+      const uint32_t bytes = NW * (kW + kTileBytes) + kx + kTileBytes;
+      int it = 0, st = 0;
+      uint32_t ph = 1;
+      bool ok = true;
+      for (int k = k_begin; k < k_end; ++k, ++it) {
+        ok = mbar_wait(smem_u32(&S.empty[st]), ph, abort_flag, p.status, 0x700 | st);
+        if (!ok) break;
         const uint32_t bar = smem_u32(&S.full[st]);
-        mbar_arrive_expect_tx(bar, C::kStageBytes);
+        mbar_arrive_expect_tx(bar, bytes);
 #pragma unroll
-        for (int w = 0; w < C::NW; ++w) {
-          tma_load_2d(smem_u32(S.w[st][w]), &p.tm_w, bar, it * BK, f0 + 128 * w);
-          tma_load_3d(smem_u32(S.ws[st][w]), &p.tm_ws, bar, 0, it, (f0 >> 7) + w);
+        for (int w = 0; w < NW; ++w) {
+          tma_load_2d(sw + (st * NW + w) * kW, &p.tm_w, bar, k * BK, f0 + 128 * w);
+          tma_load_3d(sws + (st * NW + w) * kTileBytes, &p.tm_ws, bar, 0, k, (f0 >> 7) + w);
         }
-        tma_load_2d(smem_u32(S.x[st]), &p.tm_x, bar, it * BK, m0);
-        tma_load_3d(smem_u32(S.xs[st]), &p.tm_xs, bar, 0, it, m0 >> 7);
+        tma_load_2d(sx + st * kx, &p.tm_x, bar, k * BK, m0);
+        tma_load_3d(sxs + st * kTileBytes, &p.tm_xs, bar, 0, k, m0 >> 7);
+        if (++st == c.stages) st = 0, ph ^= 1u;
       }
-      __syncwarp();
+      // every load issued lands before the CTA may exit
+      for (st = 0; !ok && st < c.stages; ++st)
+        if (it > st) mbar_wait(smem_u32(&S.full[st]), ((it - 1 - st) / c.stages) & 1u, nullptr, nullptr, 0);
     }
-    // every load issued lands before the CTA may exit
-    for (int st = 0; !ok && st < C::kStages; ++st)
-      if (it > st) mbar_wait(smem_u32(&S.full[st]), ((it - 1 - st) / C::kStages) & 1u, nullptr, nullptr, 0);
     __syncwarp();
   } else if (warp == 1) {
-    const bool leader = elect_one_sync();
-    bool ok = true;
-    for (int it = 0; it < p.kt; ++it) {
-      const int st = it % C::kStages;
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.full[st]), (it / C::kStages) & 1u, abort_flag, p.status,
-                                             0x710 | st));
-      // the scale columns of this step were last read by the MMAs of step it - 2
-      if (ok && it >= 2)
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.empty[(it - 2) % C::kStages]),
-                                               ((it - 2) / C::kStages) & 1u, abort_flag, p.status, 0x720 | st));
-      if (!ok) break;
-      tc_fence_after();
-      if (leader) {
-        const uint32_t sf = tmem + C::kScaleCol + (it & 1) * C::kSlot;
+    if (elect_one_sync()) {
+      int it = 0, st = 0, slot = 0, old = 0;
+      uint32_t ph = 0, old_ph = 0;
+      const uint32_t id = idesc(128, c.bn), sf0 = tmem + NW * c.bn;
+      for (int k = k_begin; k < k_end; ++k, ++it) {
+        bool ok = true;
+        if (it >= kNarrowSlots && c.stages > kNarrowSlots) {
+          // The scale columns of this slot were last read by the MMAs of step it - kNarrowSlots.
+          // (With fewer stages than slots the stage's own reuse waits for them.)
+          ok = mbar_wait(smem_u32(&S.empty[old]), old_ph, abort_flag, p.status, 0x720 | st);
+          if (++old == c.stages) old = 0, old_ph ^= 1u;
+        }
+        ok = ok && mbar_wait(smem_u32(&S.full[st]), ph, abort_flag, p.status, 0x710 | st);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t sf = sf0 + slot * kSlot;
 #pragma unroll
-        for (int w = 0; w < C::NW; ++w) copy_scales(sf + 4 * w, scale_desc(smem_u32(S.ws[st][w])));
-        copy_scales(sf + 4 * C::NW, scale_desc(smem_u32(S.xs[st])));
-        const uint64_t xd = operand_desc(smem_u32(S.x[st]));
-        const int blocks = min(4, (p.K - it * BK) >> 5);  // the blocks past K hold nothing
-        for (int b = 0; b < blocks; ++b)
+        for (int w = 0; w < NW; ++w) copy_scales(sf + 4 * w, scale_desc(sws + (st * NW + w) * kTileBytes));
+        copy_scales(sf + 4 * NW, scale_desc(sxs + st * kTileBytes));
+        const uint64_t wd = operand_desc(sw + st * NW * kW), xd = operand_desc(sx + st * kx);
+        const int blocks = (p.K - k * BK) >> 5;  // the blocks past K hold nothing
 #pragma unroll
-          for (int w = 0; w < C::NW; ++w)
-            mma_scaled(tmem + w * BN, operand_desc(smem_u32(S.w[st][w])) + 2 * b, xd + 2 * b,
-                       idesc(128, BN) | idesc_block(b), sf + 4 * w, sf + 4 * C::NW, it > 0 || b > 0);
+        for (int b = 0; b < 4; ++b) {
+          if (b >= blocks) break;
+#pragma unroll
+          for (int w = 0; w < NW; ++w)
+            mma_scaled(tmem + w * c.bn, wd + w * (kW >> 4) + 2 * b, xd + 2 * b, id | idesc_block(b), sf + 4 * w,
+                       sf + 4 * NW, it > 0 || b > 0);
+        }
         mma_commit(smem_u32(&S.empty[st]));
+        if (++st == c.stages) st = 0, ph ^= 1u;
+        if (++slot == kNarrowSlots) slot = 0;
       }
-      __syncwarp();
+      // also after a wait that ran out: every MMA issued completes before TMEM is released
+      mma_commit(smem_u32(&S.done));
+      mbar_wait(smem_u32(&S.done), 0, nullptr, p.status, 0x730);
     }
-    // also after a wait that ran out: every MMA issued completes before TMEM is released
-    if (leader) mma_commit(smem_u32(&S.done));
     __syncwarp();
-    mbar_wait(smem_u32(&S.done), 0, nullptr, p.status, 0x730);
-    __syncwarp();
-  } else {
-    bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.done), 0, abort_flag, p.status, 0x740));
+  }
+
+  const int lane = threadIdx.x & 31, quarter = warp & 3;
+  const int j = quarter * 32 + lane;  // feature in the block == TMEM lane
+  const int f = f0 + j, last = min(c.bn, p.M - m0);
+  const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+  bool ok = true;
+  if (warp >= 2) {
+    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.done), 0, abort_flag, p.status, 0x740));
     ok = ok && !*abort_flag;
     tc_fence_after();
-    const int quarter = warp & 3, lane = threadIdx.x & 31;
-    const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16);
-    const int j = quarter * 32 + lane;  // feature in the block == TMEM lane
-    const int f = f0 + j;
-    const int last = min(BN, p.M - m0);
-    if (ok && GATED) {
-      const int m_col = (f0 >> 1) + j;  // feature of the hidden layer
-      float bg = 0.f, bu = 0.f;
-      if (p.bias != nullptr) {
-        bg = __bfloat162float(p.bias[f]);
-        bu = __bfloat162float(p.bias[f + 128]);
-      }
-      for (int t = 0; t < last; t += 16) {
-        uint32_t g[16], u[16];
-        tmem_ld16(base + t, g);
-        tmem_ld16(base + BN + t, u);
-        tmem_wait_ld();
+  }
+
+  // What becomes of one token's sums (in the gated form y is the gate's, u the up projection's).
+  float bias = 0.f, bias_u = 0.f;
+  const bool live = GATED || f < p.N;
+  if (warp >= 2 && p.bias != nullptr && live) {
+    bias = __bfloat162float(p.bias[f]);
+    if (GATED) bias_u = __bfloat162float(p.bias[f + 128]);
+  }
+  const int seg = GATED || !live ? 0 : f / p.n_seg;
+  const int col = GATED ? (f0 >> 1) + j : f - seg * p.n_seg;
+  auto finish = [&](int t, float y, float u) {
+    const int64_t row = m0 + t;
+    if (GATED) {
+      y = silu(y + bias) * (u + bias_u);
+      // a warp's 32 features are one scale block
+      const uint32_t byte = mx_scale_byte(__reduce_max_sync(0xffffffffu, abs_bits(y)));
+      p.q[row * p.n_seg + col] = (uint8_t)mx_cvt2(y * mx_inv_scale(byte), 0.f);
+      if (lane == 0) p.scale[mx_scale_word(row, col >> 7, p.q_tile_cols) + quarter] = (uint8_t)byte;
+    } else if (live) {
+      y = activate(y + bias, p.act);
+      // read and written by the same thread: the residual may be the output
+      y = p.residual != nullptr ? fmaf(p.alpha, y, __bfloat162float(p.residual[row * p.N + f])) : y * p.alpha;
+      p.out[seg][row * p.n_seg + col] = __float2bfloat16(y);
+    }
+  };
+
+  if (c.split == 1) {
+    for (int t = 0; warp >= 2 && ok && t < last; t += 16) {
+      uint32_t v[16], u[16];
+      tmem_ld16(lanes + t, v);
+      if (GATED) tmem_ld16(lanes + c.bn + t, u);
+      tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          if (t + e >= last) break;
-          const int64_t row = m0 + t + e;
-          const float y = silu(__uint_as_float(g[e]) + bg) * (__uint_as_float(u[e]) + bu);
-          const uint32_t byte = mx_scale_byte(__reduce_max_sync(0xffffffffu, abs_bits(y)));
-          p.q[row * p.n_seg + m_col] = (uint8_t)mx_cvt2(y * mx_inv_scale(byte), 0.f);
-          if (lane == 0) p.scale[mx_scale_word(row, m_col >> 7, p.q_tile_cols) + quarter] = (uint8_t)byte;
-        }
-      }
-    } else if (ok) {
-      const bool live = f < p.N;
-      const int seg = live ? f / p.n_seg : 0;
-      const float b = live && p.bias != nullptr ? __bfloat162float(p.bias[f]) : 0.f;
-      __nv_bfloat16* out = p.out[seg] + (f - seg * p.n_seg);
-      for (int t = 0; t < last; t += 16) {
+      for (int e = 0; e < 16; ++e)
+        if (t + e < last) finish(t + e, __uint_as_float(v[e]), GATED ? __uint_as_float(u[e]) : 0.f);
+    }
+  } else {
+    // partial sums [w][token][feature], over the operands' buffers (all read by now)
+    for (int t = 0; warp >= 2 && t < last; t += 16) {
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
         uint32_t v[16];
-        tmem_ld16(base + t, v);
+        tmem_ld16(lanes + w * c.bn + t, v);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          if (t + e >= last) break;
-          const int64_t row = m0 + t + e;
-          float y = activate(__uint_as_float(v[e]) + b, p.act);
-          // read and written by the same thread: the residual may be the output
-          if (live && p.residual != nullptr)
-            y = fmaf(p.alpha, y, __bfloat162float(p.residual[row * p.N + f]));
-          else
-            y *= p.alpha;
-          if (live) out[row * p.n_seg] = __float2bfloat16(y);
-        }
+        for (int e = 0; e < 16; ++e)
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + ((w * c.bn + t + e) * 128 + j) * 4), "r"(v[e]) : "memory");
       }
     }
+    cluster_sync_all();
+    if (warp >= 2 && ok) {
+      uint32_t from[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) from[r] = cluster_addr(base, r < c.split ? r : 0) + j * 4;
+      for (int t = rank; t < last; t += c.split) {
+        float part[NW][8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+#pragma unroll
+          for (int w = 0; w < NW; ++w) part[w][r] = r < c.split ? ld_cluster_f32(from[r] + (w * c.bn + t) * 512) : 0.f;
+        float sum[NW];
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          sum[w] = part[w][0];
+#pragma unroll
+          for (int r = 1; r < 8; ++r) sum[w] += part[w][r];
+        }
+        finish(t, sum[0], sum[NW - 1]);
+      }
+    }
+    cluster_sync_all();  // nobody's partials go away while they are read
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+  if (warp == 1) tmem_dealloc(tmem, c.cols);
 }
 
 // ---------------------------------------------------------------- CTA pairs
@@ -717,18 +763,55 @@ static bool encode_out(CUtensorMap* m, const void* base, uint64_t rows, uint64_t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, bool GATED>
-static cudaError_t launch_narrow(mx::Params& p, const MxGemmArgs& a, cudaStream_t stream) {
-  using C = mx::Narrow<BN, GATED>;
-  if (!encode_values(&p.tm_x, a.x, a.M, a.K, BN) || !encode_values(&p.tm_w, a.w, a.N, a.K, 128) ||
+// Tokens per tile, stages, TMEM columns and the split of K for few tokens.
+template <bool GATED>
+static mx::Narrow narrow_config(const MxGemmArgs& a, int kt, int num_sms) {
+  constexpr int NW = GATED ? 2 : 1;
+  mx::Narrow c;
+  c.bn = a.M >= 128 ? 128 : (int)((a.M + 15) / 16) * 16;
+  const int cols = NW * c.bn + mx::kNarrowSlots * (4 * NW + 4);
+  c.cols = cols <= 256 ? 256 : 512;
+  const int stage = NW * (mx::kW + mx::kTileBytes) + c.bn * mx::BK + mx::kTileBytes;
+  const int room = (c.cols == 256 ? 110 : 220) * 1024;
+  c.stages = room / stage < mx::kNarrowMaxStages ? room / stage : mx::kNarrowMaxStages;
+  const int64_t tiles = ((a.N + NW * 128 - 1) / (NW * 128)) * ((a.M + c.bn - 1) / c.bn);
+  c.split = 1;
+  while (c.split < 8 && tiles * (c.split + 1) <= 2 * num_sms && kt >= 4 * (c.split + 1)) ++c.split;
+#ifdef QI_PROBE
+  if (getenv("QI_S")) c.split = atoi(getenv("QI_S"));
+  if (getenv("QI_ROOM")) { const int rm = atoi(getenv("QI_ROOM")) * 1024; c.stages = rm / stage < 8 ? rm / stage : 8; }
+#endif
+  const int least = (c.cols == 256 ? 76 : 152) * 1024;
+  c.smem = c.stages * stage;
+  if (c.split > 1 && c.smem < NW * c.bn * 512) c.smem = NW * c.bn * 512;  // the partial sums
+  c.smem += 1024;
+  if (c.smem < least) c.smem = least;
+  return c;
+}
+
+template <bool GATED>
+static cudaError_t launch_narrow(mx::Params& p, const MxGemmArgs& a, cudaStream_t stream, int num_sms) {
+  constexpr int NW = GATED ? 2 : 1;
+  const mx::Narrow c = narrow_config<GATED>(a, p.kt, num_sms);
+  if (!encode_values(&p.tm_x, a.x, a.M, a.K, c.bn) || !encode_values(&p.tm_w, a.w, a.N, a.K, 128) ||
       !encode_scales(&p.tm_xs, a.x_scale, a.M, a.K, 1) || !encode_scales(&p.tm_ws, a.w_scale, a.N, a.K, 1))
     return cudaErrorInvalidValue;
-  const size_t smem = sizeof(typename C::Smem) + 1024;
-  cudaError_t err = cudaFuncSetAttribute(mx::mx_gemm_narrow<BN, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+  cudaError_t err =
+      cudaFuncSetAttribute(mx::mx_gemm_narrow<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, c.smem);
   if (err != cudaSuccess) return err;
-  const dim3 grid((unsigned)((a.N + C::NW * 128 - 1) / (C::NW * 128)), (unsigned)((a.M + BN - 1) / BN));
-  mx::mx_gemm_narrow<BN, GATED><<<grid, mx::kNarrowThreads, smem, stream>>>(p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.N + NW * 128 - 1) / (NW * 128)) * c.split, (unsigned)((a.M + c.bn - 1) / c.bn));
+  cfg.blockDim = dim3(mx::kNarrowThreads);
+  cfg.dynamicSmemBytes = c.smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = c.split;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  err = cudaLaunchKernelEx(&cfg, mx::mx_gemm_narrow<GATED>, p, c);
+  if (err != cudaSuccess) return err;
   note_launch();
   return cudaGetLastError();
 }
@@ -775,7 +858,7 @@ cudaError_t launch_mx_gemm(const MxGemmArgs& a, cudaStream_t stream, int num_sms
   p.q_tile_cols = p.n_seg / 128;
   p.status = a.status;
   if (a.M > 1024) return a.gated ? launch_wide<true>(p, a, stream, num_sms) : launch_wide<false>(p, a, stream, num_sms);
-  return a.gated ? launch_narrow<128, true>(p, a, stream) : launch_narrow<128, false>(p, a, stream);
+  return a.gated ? launch_narrow<true>(p, a, stream, num_sms) : launch_narrow<false>(p, a, stream, num_sms);
 }
 
 }  // namespace qi21
