@@ -114,7 +114,7 @@ __device__ __forceinline__ float activate(float y, int act) {
 
 struct __align__(64) Params {
   CUtensorMap tm_x, tm_w, tm_xs, tm_ws;
-  CUtensorMap tm_out[kMaxOut];    // pair kernel: 32-row, 128-byte boxes of out[i], or of q
+  CUtensorMap tm_out[kMaxOut];    // pair kernel: 32-row, 64-column boxes of out[i], or of q
   int32_t tma_out;                // 1: tm_out is used
   int32_t M, N, K;
   int32_t n_seg;                  // columns per output segment (swiglu: N / 2)
@@ -412,28 +412,28 @@ __global__ void __launch_bounds__(kNarrowThreads) mx_gemm_narrow(const __grid_co
 // of X and 128 rows of W, so a CTA loads 32 KB for 128 x 256 x 128 products, two thirds of
 // what it would load alone.  Persistent: pair i walks tiles i, i + pairs, ..., M
 // fastest in groups of kGroup tiles so that pairs at work together share W and X in L2.
-//   warp 0     TMA producer of its CTA's operands (6 stages of K = 128)
+//   warp 0     TMA producer of its CTA's operands (5 stages of K = 128)
 //   warp 1     TMEM owner; in the first CTA it issues the scale copies and the MMAs
-//   warps 4-7  epilogue: one token per thread
+//   warps 4-11 epilogue: one token per thread, half of its columns
 // Tensor memory holds two accumulators of 256 columns that overlap in 64, [0, 256)
-// and [192, 448), and the scales of five K steps in the last 64.  The epilogue drains the
+// and [192, 448), and the scales of four K steps behind them.  The epilogue drains the
 // shared columns first and then lets the next tile's MMAs start, so only that
 // part of an epilogue is not hidden.
-constexpr int kWideThreads = 256;
-constexpr int kWideStages = 6;
+constexpr int kWideThreads = 384;
+constexpr int kWideStages = 5;
 constexpr int kGroup = 16;
 constexpr int kOperand = 128 * BK;
 constexpr int kWideStageBytes = 2 * kOperand + 3 * kTileBytes;
 constexpr uint32_t kAccShift = 192;
 constexpr uint32_t kWideScaleCol = 448;
-constexpr uint32_t kSlots = 5;  // of 4 (X) + 8 (W) scale columns each
+constexpr uint32_t kSlots = 4;  // of 4 (X) + 8 (W) scale columns each
 
 struct __align__(1024) WideSmem {
   uint8_t x[kWideStages][kOperand];
   uint8_t w[kWideStages][kOperand];
+  uint8_t stage[8][32 * 128];        // one 32-row box per epilogue warp (swizzled: 1024-byte aligned)
   uint8_t ws[kWideStages][2 * kTileBytes];
   uint8_t xs[kWideStages][kTileBytes];
-  uint8_t stage[4][32 * 128];        // one 32-row, 128-byte box per epilogue warp
   __nv_bfloat16 bias[2][256];        // of this tile and the next
   uint64_t full[kWideStages], empty[kWideStages];
   uint64_t acc_full[2], acc_free, drain;
@@ -463,9 +463,12 @@ __device__ __forceinline__ void add_bias(float (&y)[32], const uint32_t (&v)[32]
   }
 }
 
-// 16-byte chunk `j` (0..7) of this lane's row in a 128B-swizzled box.
+// 16-byte chunk `j` of this lane's row in a box of ROW (64 or 128) bytes a row, swizzled as the TMA's mode
+// of that width does.
+template <int ROW>
 __device__ __forceinline__ uint4* box_chunk(uint8_t* box, uint32_t lane, uint32_t j) {
-  return reinterpret_cast<uint4*>(box + lane * 128 + ((j ^ (lane & 7u)) << 4));
+  const uint32_t x = ROW == 128 ? lane & 7u : (lane >> 1) & 3u;
+  return reinterpret_cast<uint4*>(box + lane * ROW + ((j ^ x) << 4));
 }
 // The box of this warp is written: one lane hands it to the TMA.
 __device__ __forceinline__ void store_box(const CUtensorMap* map, uint8_t* box, int c0, int c1) {
@@ -501,7 +504,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     }
     mbar_init(smem_u32(&S.acc_full[0]), 1);
     mbar_init(smem_u32(&S.acc_full[1]), 1);
-    mbar_init(smem_u32(&S.acc_free), 8);  // one arrival per epilogue warp of the pair
+    mbar_init(smem_u32(&S.acc_free), 16);  // one arrival per epilogue warp of the pair
     mbar_init(smem_u32(&S.drain), 1);
     S.abort_flag = 0;
     fence_mbar_init();
@@ -520,99 +523,107 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
   const uint32_t tmem = S.tmem_base;
   const int tiles = p.mt * p.nt, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (elect_one_sync()) {
-      uint32_t it = 0, st = 0, ph = 1;
-      bool ok = true;
-      for (int t = pair; t < tiles && ok; t += pairs) {
-        int m, n;
-        tile_of(p, t, m, n);
-        const int m0 = m * 256 + (int)rank * 128, n0 = n * 256 + (int)rank * 128;
-        for (int kb = 0; kb < p.kt; ++kb, ++it) {
-          ok = mbar_wait(smem_u32(&S.empty[st]), ph, abort_flag, p.status, 0x800 | st);
-          if (!ok) break;
-          // both CTAs' bytes count on the first CTA's barrier
-          if (rank == 0) mbar_arrive_expect_tx(smem_u32(&S.full[st]), 2 * kWideStageBytes);
-          const uint32_t bar = cluster_addr(smem_u32(&S.full[st]), 0);
-          tma_load_2d_pair(smem_u32(S.x[st]), &p.tm_x, bar, kb * BK, m0);
-          tma_load_2d_pair(smem_u32(S.w[st]), &p.tm_w, bar, kb * BK, n0);
-          tma_load_3d_pair(smem_u32(S.xs[st]), &p.tm_xs, bar, 0, kb, m * 2 + (int)rank);
-          tma_load_3d_pair(smem_u32(S.ws[st]), &p.tm_ws, bar, 0, kb, n * 2);
-          if (++st == kWideStages) st = 0, ph ^= 1u;
-        }
-      }
-      if (!ok) {
-        // Loads issued must land before the CTAs may exit.  Only the first CTA's
-        // barriers see them; give the second one's the time that they need at most.
-        if (rank == 0) {
-          for (st = 0; st < kWideStages; ++st)
-            if (it > st) mbar_wait(smem_u32(&S.full[st]), ((it - 1 - st) / kWideStages) & 1u, nullptr, nullptr, 0);
-        } else {
-          const uint64_t t0 = global_ns();
-          while (global_ns() - t0 < 2000000ull) {
+  // registers: 128 x 80 + 256 x 208 of the launch's 384 x 168
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 0) {
+      // ------------------------------------------------------------ producer
+      if (elect_one_sync()) {
+        uint32_t it = 0, st = 0, ph = 1;
+        bool ok = true;
+        for (int t = pair; t < tiles && ok; t += pairs) {
+          int m, n;
+          tile_of(p, t, m, n);
+          const int m0 = m * 256 + (int)rank * 128, n0 = n * 256 + (int)rank * 128;
+          for (int kb = 0; kb < p.kt; ++kb, ++it) {
+            ok = mbar_wait(smem_u32(&S.empty[st]), ph, abort_flag, p.status, 0x800 | st);
+            if (!ok) break;
+            // both CTAs' bytes count on the first CTA's barrier
+            if (rank == 0) mbar_arrive_expect_tx(smem_u32(&S.full[st]), 2 * kWideStageBytes);
+            const uint32_t bar = cluster_addr(smem_u32(&S.full[st]), 0);
+            tma_load_2d_pair(smem_u32(S.x[st]), &p.tm_x, bar, kb * BK, m0);
+            tma_load_2d_pair(smem_u32(S.w[st]), &p.tm_w, bar, kb * BK, n0);
+            tma_load_3d_pair(smem_u32(S.xs[st]), &p.tm_xs, bar, 0, kb, m * 2 + (int)rank);
+            tma_load_3d_pair(smem_u32(S.ws[st]), &p.tm_ws, bar, 0, kb, n * 2);
+            if (++st == kWideStages) st = 0, ph ^= 1u;
           }
         }
-      }
-    }
-    __syncwarp();
-  } else if (warp == 1 && rank == 0) {
-    // ---------------------------------------------------------------- MMA
-    // One thread runs the whole loop: a stage's products take about 512 cycles, and
-    // a warp-wide loop (votes, an elected branch per stage) took longer than that.
-    if (elect_one_sync()) {
-      uint32_t it = 0, st = 0, ph = 0, slot = 0, tc = 0;
-      bool ok = true;
-      const uint64_t xd0 = operand_desc(smem_u32(S.x[0])), wd0 = operand_desc(smem_u32(S.w[0]));
-      const uint64_t xsd0 = scale_desc(smem_u32(S.xs[0])), wsd0 = scale_desc(smem_u32(S.ws[0]));
-      for (int t = pair; t < tiles && ok; t += pairs, ++tc) {
-        if (tc > 0) {  // the columns that this accumulator shares with the last one are drained
-          ok = mbar_wait_cluster(smem_u32(&S.acc_free), (tc - 1) & 1u, abort_flag, p.status, 0x810);
-          if (!ok) break;
-        }
-        const uint32_t acc = tmem + kAccShift * (tc & 1u);
-        for (int kb = 0; kb < p.kt; ++kb, ++it) {
-          // the scale columns of this slot were last read by the MMAs of step it - kSlots
-          if (it >= kSlots) {
-            const uint32_t was = it - kSlots;
-            ok = mbar_wait(smem_u32(&S.empty[was % kWideStages]), (was / kWideStages) & 1u, abort_flag, p.status,
-                           0x830 | st);
-          }
-          ok = ok && mbar_wait(smem_u32(&S.full[st]), ph, abort_flag, p.status, 0x820 | st);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t sx = tmem + kWideScaleCol + slot * 12, sw = sx + 4;
-          const uint64_t xd = xd0 + st * (kOperand >> 4), wd = wd0 + st * (kOperand >> 4);
-          const uint64_t wsd = wsd0 + st * (2 * kTileBytes >> 4);
-          copy_scales_pair(sx, xsd0 + st * (kTileBytes >> 4));
-          copy_scales_pair(sw, wsd);
-          copy_scales_pair(sw + 4, wsd + (kTileBytes >> 4));
-          const int blocks = (p.K - kb * BK) >> 5;  // the blocks past K hold nothing
-          if (blocks >= 4) {
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-              mma_scaled_pair(acc, xd + 2 * b, wd + 2 * b, idesc(256, 256) | idesc_block(b), sx, sw, kb > 0 || b > 0);
+        if (!ok) {
+          // Loads issued must land before the CTAs may exit.  Only the first CTA's
+          // barriers see them; give the second one's the time that they need at most.
+          if (rank == 0) {
+            for (st = 0; st < kWideStages; ++st)
+              if (it > st) mbar_wait(smem_u32(&S.full[st]), ((it - 1 - st) / kWideStages) & 1u, nullptr, nullptr, 0);
           } else {
-            for (int b = 0; b < blocks; ++b)
-              mma_scaled_pair(acc, xd + 2 * b, wd + 2 * b, idesc(256, 256) | idesc_block(b), sx, sw, kb > 0 || b > 0);
+            const uint64_t t0 = global_ns();
+            while (global_ns() - t0 < 2000000ull) {
+            }
           }
-          mma_commit_pair(smem_u32(&S.empty[st]));
-          if (kb == p.kt - 1) mma_commit_pair(smem_u32(&S.acc_full[tc & 1u]));
-          if (++st == kWideStages) st = 0, ph ^= 1u;
-          if (++slot == kSlots) slot = 0;
         }
       }
-      // every MMA issued completes before TMEM is released
-      mma_commit_pair(smem_u32(&S.drain));
-      mbar_wait(smem_u32(&S.drain), 0, nullptr, nullptr, 0);
+      __syncwarp();
+    } else if (warp == 1 && rank == 0) {
+      // ---------------------------------------------------------------- MMA
+      // One thread runs the whole loop: a stage's products take about 512 cycles, and
+      // a warp-wide loop (votes, an elected branch per stage) took longer than that.
+      if (elect_one_sync()) {
+        uint32_t it = 0, st = 0, ph = 0, slot = 0, tc = 0;
+        bool ok = true;
+        const uint64_t xd0 = operand_desc(smem_u32(S.x[0])), wd0 = operand_desc(smem_u32(S.w[0]));
+        const uint64_t xsd0 = scale_desc(smem_u32(S.xs[0])), wsd0 = scale_desc(smem_u32(S.ws[0]));
+        for (int t = pair; t < tiles && ok; t += pairs, ++tc) {
+          if (tc > 0) {  // the columns that this accumulator shares with the last one are drained
+            ok = mbar_wait_cluster(smem_u32(&S.acc_free), (tc - 1) & 1u, abort_flag, p.status, 0x810);
+            if (!ok) break;
+          }
+          const uint32_t acc = tmem + kAccShift * (tc & 1u);
+          for (int kb = 0; kb < p.kt; ++kb, ++it) {
+            // the scale columns of this slot were last read by the MMAs of step it - kSlots
+            if (it >= kSlots) {
+              const uint32_t was = it - kSlots;
+              ok = mbar_wait(smem_u32(&S.empty[was % kWideStages]), (was / kWideStages) & 1u, abort_flag, p.status,
+                             0x830 | st);
+            }
+            ok = ok && mbar_wait(smem_u32(&S.full[st]), ph, abort_flag, p.status, 0x820 | st);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t sx = tmem + kWideScaleCol + slot * 12, sw = sx + 4;
+            const uint64_t xd = xd0 + st * (kOperand >> 4), wd = wd0 + st * (kOperand >> 4);
+            const uint64_t wsd = wsd0 + st * (2 * kTileBytes >> 4);
+            copy_scales_pair(sx, xsd0 + st * (kTileBytes >> 4));
+            copy_scales_pair(sw, wsd);
+            copy_scales_pair(sw + 4, wsd + (kTileBytes >> 4));
+            const int blocks = (p.K - kb * BK) >> 5;  // the blocks past K hold nothing
+            if (blocks >= 4) {
+  #pragma unroll
+              for (int b = 0; b < 4; ++b)
+                mma_scaled_pair(acc, xd + 2 * b, wd + 2 * b, idesc(256, 256) | idesc_block(b), sx, sw, kb > 0 || b > 0);
+            } else {
+              for (int b = 0; b < blocks; ++b)
+                mma_scaled_pair(acc, xd + 2 * b, wd + 2 * b, idesc(256, 256) | idesc_block(b), sx, sw, kb > 0 || b > 0);
+            }
+            mma_commit_pair(smem_u32(&S.empty[st]));
+            if (kb == p.kt - 1) mma_commit_pair(smem_u32(&S.acc_full[tc & 1u]));
+            if (++st == kWideStages) st = 0, ph ^= 1u;
+            if (++slot == kSlots) slot = 0;
+          }
+        }
+        // every MMA issued completes before TMEM is released
+        mma_commit_pair(smem_u32(&S.drain));
+        mbar_wait(smem_u32(&S.drain), 0, nullptr, nullptr, 0);
+      }
+      __syncwarp();
     }
-    __syncwarp();
-  } else if (warp >= 4) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ----------------------------------------------------------- epilogue
+    // Two groups of four warps share a tile's columns: plain, group g takes columns
+    // 128 g .. 128 g + 127; gated, the gates and ups of hidden features 64 g .. 64 g + 63.
+    const int group = (warp - 4) >> 2;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t free_bar = cluster_addr(smem_u32(&S.acc_free), 0);
-    const uint32_t tid = threadIdx.x - 128, lane = threadIdx.x & 31;
-    uint8_t* box = S.stage[warp & 3];
+    const int tid = threadIdx.x & 127, lane = threadIdx.x & 31;
+    uint8_t* box = S.stage[warp - 4];
     uint32_t tc = 0;
     bool ok = true;
     for (int t = pair; t < tiles && ok; t += pairs, ++tc) {
@@ -622,54 +633,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
       const int n0 = n * 256, row0 = m * 256 + (int)rank * 128 + (warp & 3) * 32;
       const int64_t row = row0 + lane;
       const bool live = row < p.M;
-      uint32_t bias2 = 0;  // two columns each; N is even
-      if (p.bias != nullptr && n0 + 2 * (int)tid < p.N)
-        bias2 = __ldg(reinterpret_cast<const uint32_t*>(p.bias + n0) + tid);
-      reinterpret_cast<uint32_t*>(S.bias[buf])[tid] = bias2;
+      if (tid < 64) {  // this group's biases, two columns a thread (N is even)
+        const int c = GATED ? (tid < 32 ? 64 * group + 2 * tid : 64 + 64 * group + 2 * tid) : 128 * group + 2 * tid;
+        uint32_t two = 0;
+        if (p.bias != nullptr && n0 + c < p.N) two = __ldg(reinterpret_cast<const uint32_t*>(p.bias + n0 + c));
+        *reinterpret_cast<uint32_t*>(&S.bias[buf][c]) = two;
+      }
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.acc_full[buf]), (tc >> 1) & 1u, abort_flag, p.status,
                                              0x840 | buf));
       if (!ok) break;
       tc_fence_after();
       const uint32_t acc = lane_base + kAccShift * buf;
-      // The shared columns, the last 64 of buffer 0 and the first 64 of buffer 1, leave tensor memory first.
+      // The shared columns, the last 64 of buffer 0 (group 1's) and the first 64 of buffer 1
+      // (group 0's), leave tensor memory first.  A group without any arrives too: it is
+      // done with the last tile.
+      const bool holds = group != (int)buf;
       uint32_t held[2][32];
-      const uint32_t shared = buf == 0 ? 192 : 0;
-      tmem_ld32(acc + shared, held[0]);
-      tmem_ld32(acc + shared + 32, held[1]);
-      tmem_wait_ld();
+      if (holds) {
+        const uint32_t shared = buf == 0 ? 192 : 0;
+        tmem_ld32(acc + shared, held[0]);
+        tmem_ld32(acc + shared + 32, held[1]);
+        tmem_wait_ld();
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(free_bar);
-      named_bar_sync(1, 128);  // the biases are there (and the last tile's are no longer read)
-      if (GATED) reuse_box();
-      uint32_t word = 0;  // the row's four scale bytes
-      constexpr int kChunks = GATED ? 4 : 8;
+      named_bar_sync(1 + group, 128);  // the biases are there (and the last tile's are no longer read)
+      if (GATED) {
+        reuse_box();
+        uint32_t scales = 0;  // of the row's two blocks
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        // chunks in the order that uses the held columns first; gated: a held column is an
-        // up column in buffer 0, a gate column in buffer 1
-        const int c = buf == 0 ? ((i + kChunks - 2) % kChunks) * 32 : i * 32;
-        uint32_t v[32], u[32];
-        if (i < 2) {
-          if (GATED) tmem_ld32(acc + (buf == 0 ? c : 128 + c), u);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = held[i][e];
-        } else {
-          tmem_ld32(acc + c, v);
-          if (GATED) tmem_ld32(acc + 128 + c, u);
-        }
-        float y[32];
-        if (GATED) {
+        for (int i = 0; i < 2; ++i) {
+          const int c = 64 * group + 32 * i;
+          uint32_t v[32], u[32];
+          // a held column is an up column in buffer 0, a gate column in buffer 1
+          if (!(holds && buf == 1)) tmem_ld32(acc + c, v);
+          if (!(holds && buf == 0)) tmem_ld32(acc + 128 + c, u);
           tmem_wait_ld();
-          if (i < 2 && buf == 0) {
+          if (holds) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              const uint32_t x = v[e];
-              v[e] = u[e];
-              u[e] = x;
+              if (buf == 1) v[e] = held[i][e];
+              else u[e] = held[i][e];
             }
           }
-          float up[32];
+          float y[32], up[32];
           add_bias(y, v, S.bias[buf] + c);
           add_bias(up, u, S.bias[buf] + 128 + c);
           uint32_t top = 0;
@@ -680,7 +688,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
           }
           const uint32_t byte = mx_scale_byte(top);
           const float inv = mx_inv_scale(byte);
-          word |= byte << (c >> 2);
+          scales |= byte << (8 * i);
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             uint4 o;
@@ -688,18 +696,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
             o.y = mx_cvt4(y[16 * g + 4] * inv, y[16 * g + 5] * inv, y[16 * g + 6] * inv, y[16 * g + 7] * inv);
             o.z = mx_cvt4(y[16 * g + 8] * inv, y[16 * g + 9] * inv, y[16 * g + 10] * inv, y[16 * g + 11] * inv);
             o.w = mx_cvt4(y[16 * g + 12] * inv, y[16 * g + 13] * inv, y[16 * g + 14] * inv, y[16 * g + 15] * inv);
-            *box_chunk(box, lane, (c >> 4) + g) = o;
+            *box_chunk<64>(box, lane, 2 * i + g) = o;
           }
-        } else {
+        }
+        if (row0 < p.M) store_box(&p.tm_out[0], box, (n0 >> 1) + 64 * group, row0);
+        if (live)
+          *reinterpret_cast<uint16_t*>(p.scale + mx_scale_word(row, n, p.q_tile_cols) + 2 * group) = (uint16_t)scales;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // 64 columns to a box, the held ones first
+          const int c = 128 * group + (holds && group == 1 ? 32 * (i ^ 2) : 32 * i);
           if (n0 + (c & ~63) >= p.N) continue;  // (both chunks of a box alike)
+          uint32_t v[32];
+          if (!(holds && i < 2)) tmem_ld32(acc + c, v);
           uint4 res[4] = {};
           if (p.residual != nullptr && live) {
+            // read and written by the same thread: the residual may be the output
             const uint4* r = reinterpret_cast<const uint4*>(p.residual + row * p.N + n0 + c);
 #pragma unroll
             for (int g = 0; g < 4; ++g)
               if (n0 + c + 8 * g < p.N) res[g] = r[g];
           }
           tmem_wait_ld();
+          if (holds && i < 2) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = held[i & 1][e];
+          }
+          float y[32];
           add_bias(y, v, S.bias[buf] + c);
           if (p.act == QI21_ACT_SILU) {
 #pragma unroll
@@ -709,26 +733,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
             for (int e = 0; e < 32; ++e) y[e] = gelu_tanh(y[e]);
           }
           if ((i & 1) == 0 && p.tma_out) reuse_box();
+          if (p.residual != nullptr) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const uint32_t rw[4] = {res[g].x, res[g].y, res[g].z, res[g].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 rf = unpack_bf16x2(rw[e]);
+                y[8 * g + 2 * e] = fmaf(p.alpha, y[8 * g + 2 * e], rf.x);
+                y[8 * g + 2 * e + 1] = fmaf(p.alpha, y[8 * g + 2 * e + 1], rf.y);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) y[e] *= p.alpha;
+          }
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const uint32_t rw[4] = {res[g].x, res[g].y, res[g].z, res[g].w};
-            uint32_t o[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 rf = unpack_bf16x2(rw[e]);
-              float a = y[8 * g + 2 * e] * p.alpha, b = y[8 * g + 2 * e + 1] * p.alpha;
-              if (p.residual != nullptr) {
-                a = fmaf(p.alpha, y[8 * g + 2 * e], rf.x);
-                b = fmaf(p.alpha, y[8 * g + 2 * e + 1], rf.y);
-              }
-              o[e] = pack_bf16x2(a, b);
-            }
-            const uint4 ov = make_uint4(o[0], o[1], o[2], o[3]);
+            const uint4 o = make_uint4(pack_bf16x2(y[8 * g], y[8 * g + 1]), pack_bf16x2(y[8 * g + 2], y[8 * g + 3]),
+                                       pack_bf16x2(y[8 * g + 4], y[8 * g + 5]), pack_bf16x2(y[8 * g + 6], y[8 * g + 7]));
             if (p.tma_out) {
-              *box_chunk(box, lane, ((c >> 3) & 7) + g) = ov;
+              *box_chunk<128>(box, lane, 4 * (i & 1) + g) = o;
             } else if (live && n0 + c + 8 * g < p.N) {
               const int col = n0 + c + 8 * g, seg = col / p.n_seg;
-              *reinterpret_cast<uint4*>(p.out[seg] + row * p.n_seg + (col - seg * p.n_seg)) = ov;
+              *reinterpret_cast<uint4*>(p.out[seg] + row * p.n_seg + (col - seg * p.n_seg)) = o;
             }
           }
           if ((i & 1) == 1 && p.tma_out) {
@@ -737,10 +765,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
             if (row0 < p.M) store_box(&p.tm_out[seg], box, col - seg * p.n_seg, row0);
           }
         }
-      }
-      if (GATED) {
-        if (row0 < p.M) store_box(&p.tm_out[0], box, n0 >> 1, row0);
-        if (live) *reinterpret_cast<uint32_t*>(p.scale + mx_scale_word(row, n, p.q_tile_cols)) = word;
       }
     }
     reuse_box();  // the TMA has read what it was given
@@ -798,17 +822,17 @@ static bool encode_scales(CUtensorMap* m, const void* base, uint64_t rows, uint6
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 2-D map of a row-major result; boxes of 32 rows x 128 bytes, 128-byte swizzle.
+// 2-D map of a row-major result; boxes of 32 rows x 128 bytes of bf16, or 64 bytes of e4m3, swizzled.
 static bool encode_out(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t bytes) {
   auto fn = mx_encode_fn();
   if (fn == nullptr) return false;
   cuuint64_t dims[2] = {cols, rows};
   cuuint64_t strides[1] = {cols * bytes};
-  cuuint32_t box[2] = {128 / bytes, 32};
+  cuuint32_t box[2] = {64, 32};
   cuuint32_t estr[2] = {1, 1};
   return fn(m, bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            bytes == 1 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -821,15 +845,17 @@ static mx::Narrow narrow_config(const MxGemmArgs& a, int kt, int num_sms) {
   const int cols = NW * c.bn + mx::kNarrowSlots * (4 * NW + 4);
   c.cols = cols <= 256 ? 256 : 512;
   const int stage = NW * (mx::kW + mx::kTileBytes) + c.bn * mx::BK + mx::kTileBytes;
-  const int room = (c.cols == 256 ? 110 : 220) * 1024;
-  c.stages = room / stage < mx::kNarrowMaxStages ? room / stage : mx::kNarrowMaxStages;
   const int64_t tiles = ((a.N + NW * 128 - 1) / (NW * 128)) * ((a.M + c.bn - 1) / c.bn);
+  // Splitting K costs 1.4 us of cluster barriers and remote reads, and pays only while SMs would
+  // idle (measured: 16 x 4096 x 4096, 32 tiles: 13.8 us whole, 8.6 in 4 parts; 96 tiles in 2 parts:
+  // 18 -> 21 us; 128 x 4096 x 1024, 8 steps: 7.6 -> 10.4 us).  One CTA per SM takes all of its shared memory for stages
+  // (77 x 12288 x 4096 gated: 34 us with half, 25 with all); more tiles than SMs run in twos.
+  // Clusters of 8 such CTAs find room on the GPCs only while few are wanted (256 x 1024 x 4096, 16 tiles:
+  // 24 us in 8 parts; 512 x 1024, 32 tiles: 13 us in 4).
   c.split = 1;
-  while (c.split < 8 && tiles * (c.split + 1) <= 2 * num_sms && kt >= 4 * (c.split + 1)) ++c.split;
-#ifdef QI_PROBE
-  if (getenv("QI_S")) c.split = atoi(getenv("QI_S"));
-  if (getenv("QI_ROOM")) { const int rm = atoi(getenv("QI_ROOM")) * 1024; c.stages = rm / stage < 8 ? rm / stage : 8; }
-#endif
+  while (c.split < 8 && tiles * c.split * 2 <= (c.split == 4 ? 64 : num_sms) && kt >= 16 * c.split) c.split *= 2;
+  const int room = (c.cols == 256 && tiles * c.split > num_sms ? 110 : 220) * 1024;
+  c.stages = room / stage < mx::kNarrowMaxStages ? room / stage : mx::kNarrowMaxStages;
   const int least = (c.cols == 256 ? 76 : 152) * 1024;
   c.smem = c.stages * stage;
   if (c.split > 1 && c.smem < NW * c.bn * 512) c.smem = NW * c.bn * 512;  // the partial sums
@@ -870,7 +896,7 @@ static cudaError_t launch_wide(mx::Params& p, const MxGemmArgs& a, cudaStream_t 
   if (!encode_values(&p.tm_x, a.x, a.M, a.K, 128) || !encode_values(&p.tm_w, a.w, a.N, a.K, 128) ||
       !encode_scales(&p.tm_xs, a.x_scale, a.M, a.K, 1) || !encode_scales(&p.tm_ws, a.w_scale, a.N, a.K, 2))
     return cudaErrorInvalidValue;
-  // The result leaves through 32-row, 128-byte boxes, except where a segment
+  // The result leaves through 32-row, 64-column boxes, except where a segment
   // ends inside of one.
   p.tma_out = GATED || a.n_out == 1 || p.n_seg % 64 == 0;
   for (int i = 0; p.tma_out && i < a.n_out; ++i)
@@ -886,6 +912,25 @@ static cudaError_t launch_wide(mx::Params& p, const MxGemmArgs& a, cudaStream_t 
   mx::mx_gemm_wide<GATED><<<(unsigned)(2 * pairs), mx::kWideThreads, smem, stream>>>(p);
   note_launch();
   return cudaGetLastError();
+}
+
+// Which kernel for more than one tile of tokens: the estimates, in ns, are a launch plus rounds of
+// tiles over the SMs, with a K step's time in each kernel as measured (B200, us narrow / wide:
+// 512 x 4096 x 4096 18.2 / 18.4, 384 x 12288 x 4096 23 / 33, 512 x 12288 x 4096 38 / 33, 1024 x 4096 x 1024
+// 10.1 / 11.4, 1024 x 4096 x 12288 51 / 43, gated 256 x 12288 x 4096 48 / 33).
+static bool prefer_wide(const MxGemmArgs& a, int kt, int num_sms) {
+  if (a.M <= 128) return false;
+  const mx::Narrow c = a.gated ? narrow_config<true>(a, kt, num_sms) : narrow_config<false>(a, kt, num_sms);
+  const int64_t features = a.gated ? 256 : 128;
+  const int64_t ctas = ((a.N + features - 1) / features) * ((a.M + 127) / 128) * c.split;
+  const bool twos = !a.gated && ctas > num_sms;  // two CTAs to an SM
+  const int64_t per_round = twos ? 2 * num_sms : num_sms;
+  const int64_t narrow = 5000 + (c.split > 1 ? 1500 : 0) +
+                         (ctas + per_round - 1) / per_round * ((kt + c.split - 1) / c.split) *
+                             (a.gated ? 700 : twos ? 560 : 370);
+  const int64_t pairs = ((a.M + 255) / 256) * ((a.N + 255) / 256), at_once = num_sms / 2;
+  const int64_t wide = 7500 + (pairs + at_once - 1) / at_once * kt * 345;
+  return wide < narrow;
 }
 
 cudaError_t launch_mx_gemm(const MxGemmArgs& a, cudaStream_t stream, int num_sms) {
@@ -906,7 +951,8 @@ cudaError_t launch_mx_gemm(const MxGemmArgs& a, cudaStream_t stream, int num_sms
   p.scale = static_cast<uint8_t*>(a.q_scale);
   p.q_tile_cols = p.n_seg / 128;
   p.status = a.status;
-  if (a.M > 1024) return a.gated ? launch_wide<true>(p, a, stream, num_sms) : launch_wide<false>(p, a, stream, num_sms);
+  if (prefer_wide(a, p.kt, num_sms))
+    return a.gated ? launch_wide<true>(p, a, stream, num_sms) : launch_wide<false>(p, a, stream, num_sms);
   return a.gated ? launch_narrow<true>(p, a, stream, num_sms) : launch_narrow<false>(p, a, stream, num_sms);
 }
 
