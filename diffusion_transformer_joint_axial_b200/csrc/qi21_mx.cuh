@@ -19,6 +19,13 @@ constexpr uint32_t kMxNanByte = 255;
 // with infinity and then the NaNs above every finite value.
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
+// max(top, |a|, |b|) for top >= 0; a NaN anywhere gives a NaN.
+__device__ __forceinline__ float max3_abs_nan(float top, float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(top), "f"(fabsf(a)), "f"(fabsf(b)));
+  return d;
+}
+
 // Scale byte of a block whose largest abs_bits() is `bits`.  With A = m * 2^x,
 // 1 <= m < 2, and 448 = 1.75 * 2^8: e = x - 8 if m <= 1.75, else x - 7.  Adding
 // 2^21 - 1 to the bits carries into the exponent exactly when the mantissa is
