@@ -356,7 +356,8 @@ def time_denoise(qi, args, cfg, dev):
     L = sum(W.seg_tokens(s) for s in segs)
     T = W.seg_tokens(segs[-1])
     x0, ph = rnd(1, T, C), rnd(1, L - T, D)
-    model = qi.denoise.DenoiseModel(segs, H, C, nb, steps, sig, device=dev, cached=True)
+    model = qi.denoise.DenoiseModel(segs, H, C, nb, steps, sig, device=dev, cached=True,
+                                    precision=args.denoise_precision)
     model.load(params, x0, ph)
     model.run()
     model.check()
@@ -376,12 +377,14 @@ def time_denoise(qi, args, cfg, dev):
     flops = model.flops()
     del model
     torch.cuda.empty_cache()
-    full = qi.denoise.DenoiseModel(segs, H, C, nb, steps, sig, device=dev, cached=False)
+    full = qi.denoise.DenoiseModel(segs, H, C, nb, steps, sig, device=dev, cached=False,
+                                   precision=args.denoise_precision)
     full.load(params, x0, ph)
     full.run()
     full.check()
     diff = (full.x.float() - x_cached.float()).abs()
     out = {"blocks": nb, "steps": steps, "heads": H, "channels": C, "tokens": L, "target_tokens": T,
+           "precision": args.denoise_precision,
            "graph_ms_median": ms, "tflop_per_loop": flops / 1e12, "tflops": flops / (ms * 1e-3) / 1e12,
            "cached_vs_full_max_abs": float(diff.max()), "cached_vs_full_mean_abs": float(diff.mean()),
            "latent_rms": float(x_cached.float().pow(2).mean().sqrt()),
@@ -759,6 +762,8 @@ def main(argv=None):
     ap.add_argument("--denoise", action="store_true",
                     help="also time the whole denoising loop (blocks of attention + SwiGLU, 8 Euler steps)")
     ap.add_argument("--denoise-blocks", type=int, default=32)
+    ap.add_argument("--denoise-precision", choices=("bf16", "mx"), default="bf16",
+                    help="the blocks' projections and feed-forward layers of --denoise: bf16, or block-scaled 8-bit")
     ap.add_argument("--qk-norm", action="store_true",
                     help="time the variant with the QK-RMSNorm fused in front of RoPE")
     ap.add_argument("--k-rotation", default="pre-pass", choices=["pre-pass", "attention"],

@@ -15,6 +15,13 @@ the cache relies on -- the Prefix never attends the target and never sees the
 step -- holds as in the full model.  One batch element (B = 1).  Parameters
 are those of ``workloads.denoise_model`` (the oracle's ``denoise`` layout).
 
+``precision="mx"`` runs the blocks' projections and feed-forward layers in the
+block-scaled 8-bit (MX) form: weights are quantised once, when they are
+loaded; the norms and the gated projection write their results in 8 bits for
+the product that follows, and the attention's output is quantised in front of
+its projection.  The residual stream, Q, K, V, the attention, the embedding and
+the velocity head stay in bf16.
+
 This module is plumbing: it allocates buffers once and enqueues library
 calls (projections, RMSNorm, the projection with the SwiGLU gate in its
 epilogue, RoPE/cache pre-pass, attention) in stream order; every arithmetic
@@ -29,12 +36,14 @@ from .workloads import seg_tokens
 
 class DenoiseModel:
     def __init__(self, segments, heads, channels, blocks, steps, sigmas, device="cuda", cached=True,
-                 eps=1e-6):
+                 eps=1e-6, precision="bf16"):
         qb._cuda_lib()  # fails loudly without the library or a CUDA device
         if not segments or segments[-1]["kind"] != "image":
             raise qb.QI21Error(qb.QI21_ERR_INVALID_ARG, "the last segment must be the target image")
         if len(sigmas) != steps + 1:
             raise qb.QI21Error(qb.QI21_ERR_INVALID_ARG, "need steps + 1 sigmas")
+        if precision not in ("bf16", "mx"):
+            raise qb.QI21Error(qb.QI21_ERR_INVALID_ARG, "precision must be \"bf16\" or \"mx\" (got %r)" % (precision,))
         dev = torch.device(device)
         if dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
@@ -44,6 +53,7 @@ class DenoiseModel:
         self.H, self.C, self.n_blocks, self.steps = heads, channels, blocks, steps
         self.D, self.F = heads * qb.HEAD_DIM, 3 * heads * qb.HEAD_DIM
         self.sigmas, self.cached, self.eps, self.device = list(sigmas), cached, eps, dev
+        self.precision = precision
         D, F, C, L, T, P, H = self.D, self.F, self.C, self.L, self.T, self.P, self.H
         bf = torch.bfloat16
         z = lambda *shape: torch.zeros(shape, dtype=bf, device=dev)
@@ -51,8 +61,9 @@ class DenoiseModel:
         self.pos_t = self.pos[P:].clone()  # own allocation: 16-byte aligned
         # parameters
         self.w_in, self.b_in = z(D, C), z(steps, D)
-        self.blocks = [dict(norm1=z(D), w_qkv=z(3 * D, D), b_qkv=z(3 * D), w_o=z(D, D), b_o=z(D),
-                            norm2=z(D), w_gu=z(2 * F, D), b_gu=z(2 * F), w_down=z(D, F), b_down=z(D))
+        mat = z if precision == "bf16" else lambda *shape: qb.mx_empty(shape, dev)
+        self.blocks = [dict(norm1=z(D), w_qkv=mat(3 * D, D), b_qkv=z(3 * D), w_o=mat(D, D), b_o=z(D),
+                            norm2=z(D), w_gu=mat(2 * F, D), b_gu=z(2 * F), w_down=mat(D, F), b_down=z(D))
                        for _ in range(blocks)]
         self.norm_out, self.w_v, self.b_v = z(D), z(C, D), z(C)
         # inputs and state
@@ -69,8 +80,13 @@ class DenoiseModel:
     def _acts(self, n):
         z = lambda *shape: torch.zeros(shape, dtype=torch.bfloat16, device=self.device)
         D, F, H = self.D, self.F, self.H
-        return dict(h=z(1, n, D), a=z(1, n, D), q=z(1, n, H, 128), k=z(1, n, H, 128), v=z(1, n, H, 128),
-                    o=z(1, n, H, 128), m=z(1, n, F))
+        acts = dict(h=z(1, n, D), q=z(1, n, H, 128), k=z(1, n, H, 128), v=z(1, n, H, 128), o=z(1, n, H, 128))
+        if self.precision == "bf16":
+            acts.update(a=z(1, n, D), m=z(1, n, F))
+        else:  # a: also the bf16 norm in front of the velocity head; o8: the attention's output
+            mx = lambda *shape: qb.mx_empty(shape, self.device)
+            acts.update(a=z(1, n, D), a8=mx(1, n, D), o8=mx(1, n, D), m8=mx(1, n, F))
+        return acts
 
     def load(self, params, x0, prefix_h):
         """Copies parameters (``workloads.denoise_model`` layout), the initial
@@ -78,22 +94,21 @@ class DenoiseModel:
         pairs = [(self.w_in, params["w_in"]), (self.b_in, params["b_in"]), (self.norm_out, params["norm_out"]),
                  (self.w_v, params["w_v"]), (self.b_v, params["b_v"]), (self.x, x0), (self.prefix_h, prefix_h)]
         for mine, theirs in zip(self.blocks, params["blocks"]):
-            pairs += [(mine[k], theirs[k]) for k in mine]
+            pairs += [(mine[k], theirs[k]) for k in mine if isinstance(mine[k], torch.Tensor)]
         for dst, src in pairs:
             dst.copy_(src, non_blocking=True)
         # the feed-forward layer's [gate; up] weights go to the alternating
         # 128-row blocks of the fused projection + SwiGLU launch
-        for blk in self.blocks:
-            blk["w_gu"].copy_(qb.interleave_gate_up(blk["w_gu"]))
+        for blk, theirs in zip(self.blocks, params["blocks"]):
             blk["b_gu"].copy_(qb.interleave_gate_up(blk["b_gu"]))
+            if self.precision == "bf16":
+                blk["w_gu"].copy_(qb.interleave_gate_up(blk["w_gu"]))
+                continue
+            for k in ("w_qkv", "w_o", "w_gu", "w_down"):
+                w = theirs[k].to(self.device)
+                qb.mx_quantize(qb.interleave_gate_up(w) if k == "w_gu" else w, out=blk[k])
 
-    def _block(self, i, A, n):
-        """One block on the n tokens of activation set A."""
-        blk, ws = self.blocks[i], self.ws_linear
-        flat = lambda t: t.view(1, n, -1)
-        qb.rmsnorm(A["h"], blk["norm1"], self.eps, out=A["a"])
-        qb.linear(A["a"], blk["w_qkv"], blk["b_qkv"], n_out=3, out=[flat(A["q"]), flat(A["k"]), flat(A["v"])],
-                  workspace=ws)
+    def _attend(self, i, A, n):
         if n == self.L:
             kc, vc = self.caches[i] if self.cached else (None, None)
             qb.attn_full(A["q"], A["k"], A["v"], self.pos, self.kv_end, self.P, kc, vc, out=A["o"],
@@ -101,6 +116,25 @@ class DenoiseModel:
         else:
             kc, vc = self.caches[i]
             qb.attn_cached(A["q"], A["k"], A["v"], self.pos_t, kc, vc, out=A["o"], workspace=self.ws_cached)
+
+    def _block(self, i, A, n):
+        """One block on the n tokens of activation set A."""
+        blk, ws = self.blocks[i], self.ws_linear
+        flat = lambda t: t.view(1, n, -1)
+        qkv = [flat(A["q"]), flat(A["k"]), flat(A["v"])]
+        if self.precision == "mx":
+            qb.rmsnorm_mx(A["h"], blk["norm1"], self.eps, out=A["a8"])
+            qb.linear_mx(A["a8"], blk["w_qkv"], blk["b_qkv"], n_out=3, out=qkv, workspace=ws)
+            self._attend(i, A, n)
+            qb.mx_quantize(flat(A["o"]), out=A["o8"])
+            qb.linear_mx(A["o8"], blk["w_o"], blk["b_o"], residual=A["h"], out=[A["h"]], workspace=ws)
+            qb.rmsnorm_mx(A["h"], blk["norm2"], self.eps, out=A["a8"])
+            qb.linear_swiglu_mx(A["a8"], blk["w_gu"], blk["b_gu"], out=A["m8"], workspace=ws)
+            qb.linear_mx(A["m8"], blk["w_down"], blk["b_down"], residual=A["h"], out=[A["h"]], workspace=ws)
+            return
+        qb.rmsnorm(A["h"], blk["norm1"], self.eps, out=A["a"])
+        qb.linear(A["a"], blk["w_qkv"], blk["b_qkv"], n_out=3, out=qkv, workspace=ws)
+        self._attend(i, A, n)
         qb.linear_residual(flat(A["o"]), blk["w_o"], blk["b_o"], A["h"], out=A["h"], workspace=ws)
         qb.rmsnorm(A["h"], blk["norm2"], self.eps, out=A["a"])
         qb.linear_swiglu(A["a"], blk["w_gu"], blk["b_gu"], out=A["m"], workspace=ws)
