@@ -497,6 +497,7 @@ with R the product of the leading dimensions: the scale of row r and block b is
 MX_ACTIVATIONS = {"none": 0, "silu": 1, "gelu_tanh": 2, "gelu": 2}
 
 _mx_lib = None
+_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 
 
 def _mx_start(t, name):
@@ -545,13 +546,18 @@ def mx_empty(shape, device="cuda"):
 def _need_mx(t, name, shape, rows, device):
     if not isinstance(t, MXTensor):
         raise QI21Error(QI21_ERR_INVALID_ARG, "%s must be an MXTensor" % name)
-    _need(t.q, name + ".q", shape, torch.float8_e4m3fn, device)
-    _need(t.scale, name + ".scale", ((rows + 127) // 128, (shape[-1] + 127) // 128, 32, 4, 4),
-          torch.float8_e8m0fnu, device)
+    q, s = t
+    if (isinstance(q, torch.Tensor) and isinstance(s, torch.Tensor) and q.shape == shape
+            and s.shape == ((rows + 127) >> 7, (shape[-1] + 127) >> 7, 32, 4, 4) and q.dtype is _E4M3
+            and s.dtype is _E8M0 and q.device == device and s.device == device and q.is_contiguous()
+            and s.is_contiguous()):
+        return
+    _need(q, name + ".q", shape, _E4M3, device)
+    _need(s, name + ".scale", ((rows + 127) // 128, (shape[-1] + 127) // 128, 32, 4, 4), _E8M0, device)
 
 
 def _mx_operand(t, name):
-    if not isinstance(t, MXTensor):
+    if not isinstance(t, MXTensor) or not isinstance(t.q, torch.Tensor):
         raise QI21Error(QI21_ERR_INVALID_ARG, "%s must be an MXTensor" % name)
     return t.q
 
@@ -612,9 +618,10 @@ def linear_mx(x, w, bias=None, n_out=1, act="none", residual=None, alpha=1.0, ou
     n_out = 1) may be ``out[0]``."""
     xq, wq = _mx_operand(x, "x"), _mx_operand(w, "w")
     L_ = _mx_start(xq, "x.q")
-    _mx_start(wq, "w.q")
-    dev, shape, K, N = xq.device, xq.shape, _mx_matrix(xq, "x.q"), wq.shape[0]
-    R = _rows(shape)
+    dev, shape = xq.device, xq.shape
+    if len(shape) < 1 or wq.dim() != 2:
+        raise QI21Error(QI21_ERR_INVALID_ARG, "x must have rows and w two dimensions")
+    K, N, R = shape[-1], wq.shape[0], _rows(shape)
     _need_mx(x, "x", shape, R, dev)
     _need_mx(w, "w", (N, K), N, dev)
     if bias is not None:
@@ -631,8 +638,8 @@ def linear_mx(x, w, bias=None, n_out=1, act="none", residual=None, alpha=1.0, ou
         out = [torch.empty(seg, dtype=torch.bfloat16, device=dev) for _ in range(n_out)]
     if len(out) != n_out:
         raise QI21Error(QI21_ERR_INVALID_ARG, "need %d output tensors" % n_out)
-    for i, o in enumerate(out):
-        _need(o, "out[%d]" % i, seg, torch.bfloat16, dev)
+    for o in out:
+        _need(o, "out[i]", seg, torch.bfloat16, dev)
     if workspace is None:
         workspace = new_workspace(WORKSPACE_HEADER_BYTES, dev)
     _mx_call(dev, L_.qi21_linear_mx, R, N, K, xq.data_ptr(), x.scale.data_ptr(), wq.data_ptr(),
@@ -648,9 +655,10 @@ def linear_swiglu_mx(x, w_il, bias_il=None, out=None, workspace=None):
     :func:`interleave_gate_up` (interleave, then :func:`mx_quantize`); returns MX [..., F]."""
     xq, wq = _mx_operand(x, "x"), _mx_operand(w_il, "w")
     L_ = _mx_start(xq, "x.q")
-    _mx_start(wq, "w.q")
-    dev, shape, K, N = xq.device, xq.shape, _mx_matrix(xq, "x.q"), wq.shape[0]
-    R = _rows(shape)
+    dev, shape = xq.device, xq.shape
+    if len(shape) < 1 or wq.dim() != 2:
+        raise QI21Error(QI21_ERR_INVALID_ARG, "x must have rows and w two dimensions")
+    K, N, R = shape[-1], wq.shape[0], _rows(shape)
     _need_mx(x, "x", shape, R, dev)
     _need_mx(w_il, "w", (N, K), N, dev)
     if N % 256:

@@ -151,6 +151,7 @@ struct __align__(64) Params {
 constexpr int kNarrowThreads = 192;
 constexpr int kNarrowMaxStages = 8;
 constexpr int kNarrowSlots = 4;
+constexpr int kNarrowMaxSmem = 224 * 1024;
 constexpr int kW = 128 * BK;
 
 struct Narrow {
@@ -207,6 +208,8 @@ __global__ void __launch_bounds__(kNarrowThreads) mx_gemm_narrow(const __grid_co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = S.tmem_base;
+  let_next_start();
+  first_wait();
 
   if (warp == 0) {
     if (elect_one_sync()) {
@@ -488,7 +491,7 @@ __device__ __forceinline__ void reuse_box() {
 }
 
 template <bool GATED>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
+__global__ void __launch_bounds__(kWideThreads, 1)
     mx_gemm_wide(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -521,6 +524,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = S.tmem_base;
+  let_next_start();
+  first_wait();
   const int tiles = p.mt * p.nt, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   // registers: 128 x 80 + 256 x 208 of the launch's 384 x 168
@@ -871,24 +876,11 @@ static cudaError_t launch_narrow(mx::Params& p, const MxGemmArgs& a, cudaStream_
   if (!encode_values(&p.tm_x, a.x, a.M, a.K, c.bn) || !encode_values(&p.tm_w, a.w, a.N, a.K, 128) ||
       !encode_scales(&p.tm_xs, a.x_scale, a.M, a.K, 1) || !encode_scales(&p.tm_ws, a.w_scale, a.N, a.K, 1))
     return cudaErrorInvalidValue;
-  cudaError_t err =
-      cudaFuncSetAttribute(mx::mx_gemm_narrow<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, c.smem);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t err = allow_smem(mx::mx_gemm_narrow<GATED>, mx::kNarrowMaxSmem, allowed);
   if (err != cudaSuccess) return err;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.N + NW * 128 - 1) / (NW * 128)) * c.split, (unsigned)((a.M + c.bn - 1) / c.bn));
-  cfg.blockDim = dim3(mx::kNarrowThreads);
-  cfg.dynamicSmemBytes = c.smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = c.split;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  err = cudaLaunchKernelEx(&cfg, mx::mx_gemm_narrow<GATED>, p, c);
-  if (err != cudaSuccess) return err;
-  note_launch();
-  return cudaGetLastError();
+  const dim3 grid((unsigned)((a.N + NW * 128 - 1) / (NW * 128)) * c.split, (unsigned)((a.M + c.bn - 1) / c.bn));
+  return launch_dependent(mx::mx_gemm_narrow<GATED>, grid, mx::kNarrowThreads, c.smem, c.split, stream, p, c);
 }
 
 template <bool GATED>
@@ -904,14 +896,12 @@ static cudaError_t launch_wide(mx::Params& p, const MxGemmArgs& a, cudaStream_t 
   p.mt = (int32_t)((a.M + 255) / 256);
   p.nt = (int32_t)((a.N + 255) / 256);
   const size_t smem = sizeof(mx::WideSmem) + 1024;
-  cudaError_t err =
-      cudaFuncSetAttribute(mx::mx_gemm_wide<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t err = allow_smem(mx::mx_gemm_wide<GATED>, (int)smem, allowed);
   if (err != cudaSuccess) return err;
   const int64_t tiles = (int64_t)p.mt * p.nt;
   const int64_t pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;
-  mx::mx_gemm_wide<GATED><<<(unsigned)(2 * pairs), mx::kWideThreads, smem, stream>>>(p);
-  note_launch();
-  return cudaGetLastError();
+  return launch_dependent(mx::mx_gemm_wide<GATED>, dim3((unsigned)(2 * pairs)), mx::kWideThreads, smem, 2, stream, p);
 }
 
 // Which kernel for more than one tile of tokens: the estimates, in ns, are a launch plus rounds of

@@ -71,6 +71,8 @@ __device__ __forceinline__ void store_mx(const float2 (&y)[8], float top, float 
 __global__ void __launch_bounds__(256) mx_quantize_kernel(int64_t groups, int32_t K, int32_t tile_cols,
                                                           const __nv_bfloat16* __restrict__ x,
                                                           uint8_t* __restrict__ q, uint8_t* __restrict__ scale) {
+  let_next_start();
+  first_wait();
   const int64_t g = blockIdx.x * (int64_t)32 + (threadIdx.x >> 3);
   const int64_t row = g / tile_cols;
   const int32_t tc = (int32_t)(g - row * tile_cols), col = tc * 128 + (threadIdx.x & 7) * 16;
@@ -102,6 +104,8 @@ __global__ void __launch_bounds__(256) rmsnorm_mx_kernel(int64_t M, int32_t D, i
                                                          uint8_t* __restrict__ scale) {
   constexpr int kWarps = TR / 32, kKept = C > 0 ? C : 1;
   __shared__ float part[8];
+  let_next_start();
+  first_wait();
   const int t = threadIdx.x % TR;
   const int64_t row = blockIdx.x * (int64_t)(256 / TR) + threadIdx.x / TR;
   const int pieces = row < M ? D / 16 : 0;  // (whole warps have none)
@@ -204,14 +208,14 @@ __global__ void __launch_bounds__(256) rmsnorm_mx_kernel(int64_t M, int32_t D, i
 }
 
 template <int TR, int C>
-void run_rmsnorm_mx(int64_t M, int32_t D, const void* x, const void* delta, const void* w, float eps, void* sum,
-                    void* q, void* scale, cudaStream_t stream) {
+cudaError_t run_rmsnorm_mx(int64_t M, int32_t D, const void* x, const void* delta, const void* w, float eps,
+                           void* sum, void* q, void* scale, cudaStream_t stream) {
   constexpr int kRows = 256 / TR;
-  auto kernel = delta != nullptr ? rmsnorm_mx_kernel<TR, C, true> : rmsnorm_mx_kernel<TR, C, false>;
-  kernel<<<(unsigned)((M + kRows - 1) / kRows), 256, 0, stream>>>(
-      M, D, (D + 127) / 128, static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(delta),
-      static_cast<const __nv_bfloat16*>(w), eps, static_cast<__nv_bfloat16*>(sum), static_cast<uint8_t*>(q),
-      static_cast<uint8_t*>(scale));
+  return launch_dependent(delta != nullptr ? rmsnorm_mx_kernel<TR, C, true> : rmsnorm_mx_kernel<TR, C, false>,
+                          dim3((unsigned)((M + kRows - 1) / kRows)), 256, 0, 1, stream, M, D, (D + 127) / 128,
+                          static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(delta),
+                          static_cast<const __nv_bfloat16*>(w), eps, static_cast<__nv_bfloat16*>(sum),
+                          static_cast<uint8_t*>(q), static_cast<uint8_t*>(scale));
 }
 
 }  // namespace
@@ -220,11 +224,9 @@ cudaError_t launch_mx_quantize(int64_t M, int64_t K, const void* x, void* q, voi
   if (M == 0 || K == 0) return cudaSuccess;
   const int32_t tile_cols = (int32_t)((K + 127) / 128);
   const int64_t groups = M * tile_cols;
-  mx_quantize_kernel<<<(unsigned)((groups + 31) / 32), 256, 0, stream>>>(
-      groups, (int32_t)K, tile_cols, static_cast<const __nv_bfloat16*>(x), static_cast<uint8_t*>(q),
-      static_cast<uint8_t*>(scale));
-  note_launch();
-  return cudaGetLastError();
+  return launch_dependent(mx_quantize_kernel, dim3((unsigned)((groups + 31) / 32)), 256, 0, 1, stream, groups,
+                          (int32_t)K, tile_cols, static_cast<const __nv_bfloat16*>(x), static_cast<uint8_t*>(q),
+                          static_cast<uint8_t*>(scale));
 }
 
 cudaError_t launch_rmsnorm_mx(int64_t M, int32_t D, const void* x, const void* delta, const void* w, float eps,
@@ -245,9 +247,7 @@ cudaError_t launch_rmsnorm_mx(int64_t M, int32_t D, const void* x, const void* d
              : pieces <= 512 ? run_rmsnorm_mx<256, 2>
              : pieces <= 768 ? run_rmsnorm_mx<256, 3>
                              : run_rmsnorm_mx<256, 0>;
-  run(M, D, x, delta, w, eps, sum, q, scale, stream);
-  note_launch();
-  return cudaGetLastError();
+  return run(M, D, x, delta, w, eps, sum, q, scale, stream);
 }
 
 }  // namespace qi21

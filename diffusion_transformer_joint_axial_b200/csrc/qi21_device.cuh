@@ -215,6 +215,16 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
       : "memory");
 }
 
+// ------------------------------------------- dependent launches of a stream
+// A kernel launched with launch_dependent() may start while the kernel in front
+// of it still runs.  first_wait() returns when that kernel (and so every one before it) has
+// completed and its writes are visible: nothing in global memory is touched
+// before.  let_next_start() allows the following kernel the same from here on;
+// it takes effect once every CTA has called it, so all CTAs of this grid are on
+// their SMs by then.
+__device__ __forceinline__ void first_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ------------------------------------------------- CTA pairs and clusters
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;

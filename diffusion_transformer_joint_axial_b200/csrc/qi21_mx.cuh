@@ -9,6 +9,8 @@
 // NaN, and a product with it is NaN.
 #pragma once
 
+#include <atomic>
+
 #include "qi21_device.cuh"
 
 namespace qi21 {
@@ -60,6 +62,45 @@ __device__ __forceinline__ uint32_t mx_cvt4(float a, float b, float c, float d) 
 // the four bytes of a row in one tile.
 __host__ __device__ __forceinline__ int64_t mx_scale_word(int64_t row, int64_t tile_col, int64_t tile_cols) {
   return ((row >> 7) * tile_cols + tile_col) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
+}
+
+// Launches `kernel` so that its start may overlap the end of the kernel in front of
+// it in the stream (see first_wait()); `cluster` > 1: clusters of that many CTAs
+// along x.  Repeated calls of 20 us kernels ran 2 us apart closer for it.
+template <typename... P, typename... A>
+inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster,
+                                    cudaStream_t stream, const A&... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) return e;
+  note_launch();
+  return cudaGetLastError();
+}
+
+// Raises `kernel`'s dynamic shared memory limit to `bytes` on the current device,
+// once for each (the call costs half a microsecond).
+template <typename K>
+inline cudaError_t allow_smem(K* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 }  // namespace qi21
