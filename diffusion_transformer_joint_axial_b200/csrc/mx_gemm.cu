@@ -466,6 +466,15 @@ __device__ __forceinline__ void add_bias(float (&y)[32], const uint32_t (&v)[32]
   }
 }
 
+// Adds the sums of 32 columns in another CTA's shared memory, 512 bytes apart.
+__device__ __forceinline__ void add_others(uint32_t (&v)[32], uint32_t from) {
+  float o[32];
+#pragma unroll
+  for (int e = 0; e < 32; ++e) o[e] = ld_cluster_f32(from + e * 512);
+#pragma unroll
+  for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + o[e]);
+}
+
 // 16-byte chunk `j` of this lane's row in a box of ROW (64 or 128) bytes a row, swizzled as the TMA's mode
 // of that width does.
 template <int ROW>
@@ -490,15 +499,20 @@ __device__ __forceinline__ void reuse_box() {
   __syncwarp();
 }
 
-template <bool GATED>
-__global__ void __launch_bounds__(kWideThreads, 1)
-    mx_gemm_wide(const __grid_constant__ Params p) {
+//
+// SPLIT: one tile to a cluster of two pairs, each with half of K, for calls with few tiles.  When
+// both are done, the pairs swap halves of the tile's columns through shared
+// memory (fp32, [column][token]): pair i finishes what group i of its epilogue warps
+// holds, adding the other pair's sums to its own.
+template <bool GATED, bool SPLIT>
+__global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   WideSmem& S = *reinterpret_cast<WideSmem*>(smem_raw + (((raw + 1023u) & ~1023u) - raw));
   const int warp = threadIdx.x >> 5;
   volatile int* abort_flag = &S.abort_flag;
-  const uint32_t rank = cluster_rank();
+  const uint32_t rank = cluster_rank() & 1u, first = cluster_rank() & ~1u;  // in the pair; the pair's first CTA
+  const int part = SPLIT ? (int)(cluster_rank() >> 1) : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kWideStages; ++s) {
@@ -526,7 +540,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const uint32_t tmem = S.tmem_base;
   let_next_start();
   first_wait();
-  const int tiles = p.mt * p.nt, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int tiles = p.mt * p.nt, pair = blockIdx.x >> (SPLIT ? 2 : 1), pairs = gridDim.x >> (SPLIT ? 2 : 1);
+  const int k_begin = SPLIT && part == 1 ? p.kt / 2 : 0, k_end = SPLIT && part == 0 ? p.kt / 2 : p.kt;
 
   // registers: 128 x 80 + 256 x 208 of the launch's 384 x 168
   if (warp < 4) {
@@ -540,12 +555,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           int m, n;
           tile_of(p, t, m, n);
           const int m0 = m * 256 + (int)rank * 128, n0 = n * 256 + (int)rank * 128;
-          for (int kb = 0; kb < p.kt; ++kb, ++it) {
+          for (int kb = k_begin; kb < k_end; ++kb, ++it) {
             ok = mbar_wait(smem_u32(&S.empty[st]), ph, abort_flag, p.status, 0x800 | st);
             if (!ok) break;
             // both CTAs' bytes count on the first CTA's barrier
             if (rank == 0) mbar_arrive_expect_tx(smem_u32(&S.full[st]), 2 * kWideStageBytes);
-            const uint32_t bar = cluster_addr(smem_u32(&S.full[st]), 0);
+            const uint32_t bar = cluster_addr(smem_u32(&S.full[st]), first);
             tma_load_2d_pair(smem_u32(S.x[st]), &p.tm_x, bar, kb * BK, m0);
             tma_load_2d_pair(smem_u32(S.w[st]), &p.tm_w, bar, kb * BK, n0);
             tma_load_3d_pair(smem_u32(S.xs[st]), &p.tm_xs, bar, 0, kb, m * 2 + (int)rank);
@@ -582,7 +597,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             if (!ok) break;
           }
           const uint32_t acc = tmem + kAccShift * (tc & 1u);
-          for (int kb = 0; kb < p.kt; ++kb, ++it) {
+          for (int kb = k_begin; kb < k_end; ++kb, ++it) {
             // the scale columns of this slot were last read by the MMAs of step it - kSlots
             if (it >= kSlots) {
               const uint32_t was = it - kSlots;
@@ -602,23 +617,24 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             if (blocks >= 4) {
   #pragma unroll
               for (int b = 0; b < 4; ++b)
-                mma_scaled_pair(acc, xd + 2 * b, wd + 2 * b, idesc(256, 256) | idesc_block(b), sx, sw, kb > 0 || b > 0);
+                mma_scaled_pair(acc, xd + 2 * b, wd + 2 * b, idesc(256, 256) | idesc_block(b), sx, sw, kb > k_begin || b > 0);
             } else {
               for (int b = 0; b < blocks; ++b)
-                mma_scaled_pair(acc, xd + 2 * b, wd + 2 * b, idesc(256, 256) | idesc_block(b), sx, sw, kb > 0 || b > 0);
+                mma_scaled_pair(acc, xd + 2 * b, wd + 2 * b, idesc(256, 256) | idesc_block(b), sx, sw, kb > k_begin || b > 0);
             }
-            mma_commit_pair(smem_u32(&S.empty[st]));
-            if (kb == p.kt - 1) mma_commit_pair(smem_u32(&S.acc_full[tc & 1u]));
+            mma_commit_pair(smem_u32(&S.empty[st]), first);
+            if (kb == k_end - 1) mma_commit_pair(smem_u32(&S.acc_full[tc & 1u]), first);
             if (++st == kWideStages) st = 0, ph ^= 1u;
             if (++slot == kSlots) slot = 0;
           }
         }
         // every MMA issued completes before TMEM is released
-        mma_commit_pair(smem_u32(&S.drain));
+        mma_commit_pair(smem_u32(&S.drain), first);
         mbar_wait(smem_u32(&S.drain), 0, nullptr, nullptr, 0);
       }
       __syncwarp();
     }
+    if (SPLIT) cluster_sync_all();  // the sums are there
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ----------------------------------------------------------- epilogue
@@ -626,7 +642,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     // 128 g .. 128 g + 127; gated, the gates and ups of hidden features 64 g .. 64 g + 63.
     const int group = (warp - 4) >> 2;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t free_bar = cluster_addr(smem_u32(&S.acc_free), 0);
+    const uint32_t free_bar = cluster_addr(smem_u32(&S.acc_free), first);
     const int tid = threadIdx.x & 127, lane = threadIdx.x & 31;
     uint8_t* box = S.stage[warp - 4];
     uint32_t tc = 0;
@@ -646,13 +662,16 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       }
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.acc_full[buf]), (tc >> 1) & 1u, abort_flag, p.status,
                                              0x840 | buf));
-      if (!ok) break;
+      if (!ok) {
+        if (SPLIT) cluster_sync_all();
+        break;
+      }
       tc_fence_after();
       const uint32_t acc = lane_base + kAccShift * buf;
       // The shared columns, the last 64 of buffer 0 (group 1's) and the first 64 of buffer 1
       // (group 0's), leave tensor memory first.  A group without any arrives too: it is
       // done with the last tile.
-      const bool holds = group != (int)buf;
+      const bool holds = !SPLIT && group != (int)buf;
       uint32_t held[2][32];
       if (holds) {
         const uint32_t shared = buf == 0 ? 192 : 0;
@@ -662,8 +681,27 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(free_bar);
+      if (!SPLIT && lane == 0) mbar_arrive_cluster(free_bar);
       named_bar_sync(1 + group, 128);  // the biases are there (and the last tile's are no longer read)
+      uint32_t others = 0;  // the other pair's sums of this thread's token and this group's first column
+      if (SPLIT) {
+        const uint32_t mine = smem_u32(S.x[0]) + ((warp & 3) * 32 + lane) * 4;
+        if (group != part) {
+          // this group's columns: plain 128; gated 64 gates, then 64 ups
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t v[32];
+            tmem_ld32(acc + (GATED ? (i < 2 ? 64 * group + 32 * i : 64 + 64 * group + 32 * i) : 128 * group + 32 * i), v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(mine + (32 * i + e) * 512), "r"(v[e]) : "memory");
+          }
+        }
+        cluster_sync_all();
+        if (group != part) break;  // the other pair finishes these
+        others = cluster_addr(mine, cluster_rank() ^ 2u);
+      }
       if (GATED) {
         reuse_box();
         uint32_t scales = 0;  // of the row's two blocks
@@ -675,6 +713,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if (!(holds && buf == 1)) tmem_ld32(acc + c, v);
           if (!(holds && buf == 0)) tmem_ld32(acc + 128 + c, u);
           tmem_wait_ld();
+          if (SPLIT) {
+            add_others(v, others + 32 * i * 512);
+            add_others(u, others + (64 + 32 * i) * 512);
+          }
           if (holds) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
@@ -724,6 +766,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
               if (n0 + c + 8 * g < p.N) res[g] = r[g];
           }
           tmem_wait_ld();
+          if (SPLIT) add_others(v, others + 32 * i * 512);
           if (holds && i < 2) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = held[i & 1][e];
@@ -883,7 +926,7 @@ static cudaError_t launch_narrow(mx::Params& p, const MxGemmArgs& a, cudaStream_
   return launch_dependent(mx::mx_gemm_narrow<GATED>, grid, mx::kNarrowThreads, c.smem, c.split, stream, p, c);
 }
 
-template <bool GATED>
+template <bool GATED, bool SPLIT>
 static cudaError_t launch_wide(mx::Params& p, const MxGemmArgs& a, cudaStream_t stream, int num_sms) {
   if (!encode_values(&p.tm_x, a.x, a.M, a.K, 128) || !encode_values(&p.tm_w, a.w, a.N, a.K, 128) ||
       !encode_scales(&p.tm_xs, a.x_scale, a.M, a.K, 1) || !encode_scales(&p.tm_ws, a.w_scale, a.N, a.K, 2))
@@ -897,30 +940,39 @@ static cudaError_t launch_wide(mx::Params& p, const MxGemmArgs& a, cudaStream_t 
   p.nt = (int32_t)((a.N + 255) / 256);
   const size_t smem = sizeof(mx::WideSmem) + 1024;
   static std::atomic<uint64_t> allowed{0};
-  cudaError_t err = allow_smem(mx::mx_gemm_wide<GATED>, (int)smem, allowed);
+  cudaError_t err = allow_smem(mx::mx_gemm_wide<GATED, SPLIT>, (int)smem, allowed);
   if (err != cudaSuccess) return err;
   const int64_t tiles = (int64_t)p.mt * p.nt;
   const int64_t pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;
-  return launch_dependent(mx::mx_gemm_wide<GATED>, dim3((unsigned)(2 * pairs)), mx::kWideThreads, smem, 2, stream, p);
+  const int cluster = SPLIT ? 4 : 2;
+  return launch_dependent(mx::mx_gemm_wide<GATED, SPLIT>, dim3((unsigned)(cluster * pairs)), mx::kWideThreads, smem,
+                          cluster, stream, p);
 }
 
+enum class Way { kNarrow, kWide, kSplit };
+
 // Which kernel for more than one tile of tokens: the estimates, in ns, are a launch plus rounds of
-// tiles over the SMs, with a K step's time in each kernel as measured (B200, us narrow / wide:
-// 512 x 4096 x 4096 18.2 / 18.4, 384 x 12288 x 4096 23 / 33, 512 x 12288 x 4096 38 / 33, 1024 x 4096 x 1024
-// 10.1 / 11.4, 1024 x 4096 x 12288 51 / 43, gated 256 x 12288 x 4096 48 / 33).
-static bool prefer_wide(const MxGemmArgs& a, int kt, int num_sms) {
-  if (a.M <= 128) return false;
+// tiles over the SMs, with a K step's time in each kernel as measured (B200, us, narrow / pairs /
+// pairs with K split: 512 x 4096 x 4096 16.7 / 17.6 / 15.6, 512 x 4096 x 12288 39 / 38 / 27,
+// 1024 x 4096 x 2048 12.2 / 13.4 / -, 1024 x 4096 x 12288 49 / 42 / -, 2048 x 4096 x 4096 38 / 31 / -; gated
+// 333 x 2048 x 4096 20 / 16 / 13, 1000 x 4096 x 4096 44 / 30 / -).
+static Way choose(const MxGemmArgs& a, int kt, int num_sms) {
+  if (a.M <= 128) return Way::kNarrow;
+  if (a.M > 128 * 65535ll) return Way::kWide;  // more token tiles than a grid's second axis takes
   const mx::Narrow c = a.gated ? narrow_config<true>(a, kt, num_sms) : narrow_config<false>(a, kt, num_sms);
   const int64_t features = a.gated ? 256 : 128;
   const int64_t ctas = ((a.N + features - 1) / features) * ((a.M + 127) / 128) * c.split;
   const bool twos = !a.gated && ctas > num_sms;  // two CTAs to an SM
   const int64_t per_round = twos ? 2 * num_sms : num_sms;
-  const int64_t narrow = 5000 + (c.split > 1 ? 1500 : 0) +
+  const int64_t narrow = 5000 + (c.split == 1 ? 0 : a.gated ? 6000 : 1500) +
                          (ctas + per_round - 1) / per_round * ((kt + c.split - 1) / c.split) *
                              (a.gated ? 700 : twos ? 560 : 370);
-  const int64_t pairs = ((a.M + 255) / 256) * ((a.N + 255) / 256), at_once = num_sms / 2;
-  const int64_t wide = 7500 + (pairs + at_once - 1) / at_once * kt * 345;
-  return wide < narrow;
+  const int64_t tiles = ((a.M + 255) / 256) * ((a.N + 255) / 256), at_once = num_sms / 2;
+  const int64_t wide = 7500 + (tiles + at_once - 1) / at_once * kt * 345;
+  // (of 37 clusters of four CTAs, one CTA to an SM, not all found room at once; 32 did)
+  const int64_t split = 4 * tiles <= num_sms - 20 && kt >= 8 ? 9500 + (kt + 1) / 2 * 345 : INT64_MAX;
+  if (split < narrow && split < wide) return Way::kSplit;
+  return wide < narrow ? Way::kWide : Way::kNarrow;
 }
 
 cudaError_t launch_mx_gemm(const MxGemmArgs& a, cudaStream_t stream, int num_sms) {
@@ -941,8 +993,11 @@ cudaError_t launch_mx_gemm(const MxGemmArgs& a, cudaStream_t stream, int num_sms
   p.scale = static_cast<uint8_t*>(a.q_scale);
   p.q_tile_cols = p.n_seg / 128;
   p.status = a.status;
-  if (prefer_wide(a, p.kt, num_sms))
-    return a.gated ? launch_wide<true>(p, a, stream, num_sms) : launch_wide<false>(p, a, stream, num_sms);
+  const Way way = choose(a, p.kt, num_sms);
+  if (way == Way::kWide)
+    return a.gated ? launch_wide<true, false>(p, a, stream, num_sms) : launch_wide<false, false>(p, a, stream, num_sms);
+  if (way == Way::kSplit)
+    return a.gated ? launch_wide<true, true>(p, a, stream, num_sms) : launch_wide<false, true>(p, a, stream, num_sms);
   return a.gated ? launch_narrow<true>(p, a, stream, num_sms) : launch_narrow<false>(p, a, stream, num_sms);
 }
 

@@ -254,12 +254,12 @@ __device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncol
 __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
-// Arrives once on `bar` of both CTAs when every tcgen05 operation of the pair
-// that this thread issued before has completed.
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+// Arrives once on `bar` of both CTAs of the pair (`first`: the cluster rank of
+// its first) when every tcgen05 operation that this thread issued before has completed.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint32_t first) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"((uint16_t)3)
+      "h"((uint16_t)(3u << first))
       : "memory");
 }
 

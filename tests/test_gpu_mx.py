@@ -208,6 +208,9 @@ SHAPES = [
     (1000, 20480, 160, 4, True, "none", False),     # many column tiles
     (2049, 2056, 96, 1, True, "none", True),        # ragged in M, N and K past the large tiles
     (4352, 1536, 1024, 1, True, "silu", True),
+    (333, 4096, 4096, 1, True, "gelu_tanh", False),  # few large tiles: K in two halves
+    (1000, 2056, 4128, 1, True, "none", True),       # the same, ragged everywhere
+    (513, 3 * 808, 3968, 3, True, "silu", False),    # segments that end inside of a box
 ]
 
 
@@ -228,7 +231,8 @@ def test_linear_mx(cuda_device, M, N, K, n_out, bias, act, residual):
 
 
 @pytest.mark.parametrize("M,F,K", [(1, 128, 32), (1, 1536, 4096), (5, 256, 96), (16, 384, 160), (33, 640, 1056), (77, 1024, 512),
-                                   (129, 256, 320), (300, 1152, 1024), (1000, 2304, 672), (2500, 3200, 512)])
+                                   (129, 256, 320), (300, 1152, 1024), (1000, 2304, 672), (2500, 3200, 512),
+                                   (300, 2048, 4096), (700, 1152, 3104)])
 def test_linear_swiglu_mx(cuda_device, M, F, K):
     rng = np.random.default_rng(M + F + K)
     x, xv = _mx_operand(rng, M, K, 1.0, cuda_device)
