@@ -70,15 +70,15 @@ __device__ __forceinline__ bool mbar_try_wait_sleep(uint32_t bar, uint32_t parit
   return ok != 0;
 }
 
-// mbar_try_wait_sleep() that also acquires what other CTAs of the cluster released.
-__device__ __forceinline__ bool mbar_try_wait_sleep_cluster(uint32_t bar, uint32_t parity, uint32_t ns) {
+// mbar_try_wait() on a barrier of arrivals made with mbar_arrive_cluster().
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(ns)
+      : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
 }
@@ -106,22 +106,23 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
-// mbar_wait() on a barrier at which threads of other CTAs of the cluster arrive.
+// mbar_wait() on such a barrier.  It polls: for single threads on the critical path.
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort,
                                                   uint32_t* status, uint32_t where,
                                                   uint64_t limit_ns = kWaitLimitNs) {
-  uint64_t t0 = 0;
-  while (!mbar_try_wait_sleep_cluster(bar, parity, 1000u)) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait_cluster(bar, parity)) return true;
     if (abort != nullptr && *abort) return false;
-    const uint64_t t = global_ns();
-    if (t0 == 0) t0 = t;
-    if (t - t0 > limit_ns) {
+    if (global_ns() - t0 > limit_ns) {
       if (abort != nullptr) *abort = 1;
       record_status(status, kStatusTimeout, where);
       return false;
     }
   }
-  return true;
 }
 
 // ----------------------------------------------------------------------- TMA
@@ -242,8 +243,11 @@ __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Arrives at a barrier of another CTA of the cluster, with no order for memory: for handing over tensor
+// memory, between tc_fence_before() here and tc_fence_after() behind the wait.  (A
+// release at cluster scope waited for every earlier store of the thread, 1600 cycles.)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 // TMEM of both CTAs of a pair: one warp in each of the two executes these.
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
