@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kNarrowThreads) mx_gemm_narrow(const __grid_co
       }
       finish(t, n, y, u);
     }
-    cluster_sync_all();  // nobody's partials go away while they are read
+    cluster_sync_exit();  // nobody's partials go away while they are read
   }
   tc_fence_before();
   __syncthreads();
@@ -820,7 +820,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
 
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();
+  cluster_sync_exit();
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }

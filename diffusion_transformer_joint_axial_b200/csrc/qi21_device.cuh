@@ -243,6 +243,12 @@ __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same without an order for memory: before leaving, so that no CTA's shared memory goes while others
+// still use it.  (Ordered, it would wait for the results' stores.)
+__device__ __forceinline__ void cluster_sync_exit() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
 // Arrives at a barrier of another CTA of the cluster, with no order for memory: for handing over tensor
 // memory, between tc_fence_before() here and tc_fence_after() behind the wait.  (A
 // release at cluster scope waited for every earlier store of the thread, 1600 cycles.)
