@@ -114,7 +114,7 @@ __device__ __forceinline__ float activate(float y, int act) {
 
 struct __align__(64) Params {
   CUtensorMap tm_x, tm_w, tm_xs, tm_ws;
-  CUtensorMap tm_out[kMaxOut];    // pair kernel: 32-row, 64-column boxes of out[i], or of q
+  CUtensorMap tm_out[kMaxOut];    // pair kernel: 32-row, 64-byte boxes of out[i], or of q
   int32_t tma_out;                // 1: tm_out is used
   int32_t M, N, K;
   int32_t n_seg;                  // columns per output segment (swiglu: N / 2)
@@ -434,10 +434,10 @@ constexpr uint32_t kSlots = 4;  // of 4 (X) + 8 (W) scale columns each
 struct __align__(1024) WideSmem {
   uint8_t x[kWideStages][kOperand];
   uint8_t w[kWideStages][kOperand];
-  uint8_t stage[8][32 * 128];        // one 32-row box per epilogue warp (swizzled: 1024-byte aligned)
+  uint8_t stage[8][2][32 * 64];      // two boxes per epilogue warp (swizzled: 512-byte aligned)
   uint8_t ws[kWideStages][2 * kTileBytes];
   uint8_t xs[kWideStages][kTileBytes];
-  __nv_bfloat16 bias[2][256];        // of this tile and the next
+  float bias[2][256];                // of this tile and the next
   uint64_t full[kWideStages], empty[kWideStages];
   uint64_t acc_full[2], acc_free, drain;
   uint32_t tmem_base;
@@ -452,17 +452,14 @@ __device__ __forceinline__ void tile_of(const Params& p, int t, int& m, int& n) 
 }
 
 // 32 accumulators plus their biases (in shared memory, the same for every thread).
-__device__ __forceinline__ void add_bias(float (&y)[32], const uint32_t (&v)[32], const __nv_bfloat16* bias) {
+__device__ __forceinline__ void add_bias(float (&y)[32], const uint32_t (&v)[32], const float* bias) {
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const uint4 b = reinterpret_cast<const uint4*>(bias)[g];
-    const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = unpack_bf16x2(bw[e]);
-      y[8 * g + 2 * e] = __uint_as_float(v[8 * g + 2 * e]) + f.x;
-      y[8 * g + 2 * e + 1] = __uint_as_float(v[8 * g + 2 * e + 1]) + f.y;
-    }
+  for (int g = 0; g < 8; ++g) {
+    const float4 b = reinterpret_cast<const float4*>(bias)[g];
+    y[4 * g] = __uint_as_float(v[4 * g]) + b.x;
+    y[4 * g + 1] = __uint_as_float(v[4 * g + 1]) + b.y;
+    y[4 * g + 2] = __uint_as_float(v[4 * g + 2]) + b.z;
+    y[4 * g + 3] = __uint_as_float(v[4 * g + 3]) + b.w;
   }
 }
 
@@ -475,12 +472,10 @@ __device__ __forceinline__ void add_others(uint32_t (&v)[32], uint32_t from) {
   for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + o[e]);
 }
 
-// 16-byte chunk `j` of this lane's row in a box of ROW (64 or 128) bytes a row, swizzled as the TMA's mode
-// of that width does.
-template <int ROW>
+// A warp's results leave through boxes of 32 rows x 64 bytes, swizzled as the TMA's
+// 64-byte mode does.  16-byte chunk `j` of this lane's row:
 __device__ __forceinline__ uint4* box_chunk(uint8_t* box, uint32_t lane, uint32_t j) {
-  const uint32_t x = ROW == 128 ? lane & 7u : (lane >> 1) & 3u;
-  return reinterpret_cast<uint4*>(box + lane * ROW + ((j ^ x) << 4));
+  return reinterpret_cast<uint4*>(box + lane * 64 + ((j ^ ((lane >> 1) & 3u)) << 4));
 }
 // The box of this warp is written: one lane hands it to the TMA.
 __device__ __forceinline__ void store_box(const CUtensorMap* map, uint8_t* box, int c0, int c1) {
@@ -493,9 +488,10 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, uint8_t* box, 
     bulk_commit_group();
   }
 }
-// ... and may be written again once the TMA has read it.
+// A warp has two boxes and uses them in turn: the one before the last store's may be
+// written again once the TMA has read it.
 __device__ __forceinline__ void reuse_box() {
-  if (elect_one_sync()) bulk_wait_read_all();
+  if (elect_one_sync()) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
   __syncwarp();
 }
 
@@ -644,9 +640,18 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t free_bar = cluster_addr(smem_u32(&S.acc_free), first);
     const int tid = threadIdx.x & 127, lane = threadIdx.x & 31;
-    uint8_t* box = S.stage[warp - 4];
+    uint32_t boxes = 0;  // stored so far
     uint32_t tc = 0;
     bool ok = true;
+    // Each thread brings one of its group's 128 biases a tile, requested a tile ahead.
+    const int bias_col = GATED ? (tid < 64 ? 64 * group + tid : 64 + 64 * group + tid) : 128 * group + tid;
+    auto load_bias = [&](int t) {
+      int m, n;
+      tile_of(p, t, m, n);
+      const int c = n * 256 + bias_col;
+      return p.bias != nullptr && c < p.N ? __bfloat162float(p.bias[c]) : 0.f;
+    };
+    float next_bias = pair < tiles ? load_bias(pair) : 0.f;
     for (int t = pair; t < tiles && ok; t += pairs, ++tc) {
       const uint32_t buf = tc & 1u;
       int m, n;
@@ -654,12 +659,21 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
       const int n0 = n * 256, row0 = m * 256 + (int)rank * 128 + (warp & 3) * 32;
       const int64_t row = row0 + lane;
       const bool live = row < p.M;
-      if (tid < 64) {  // this group's biases, two columns a thread (N is even)
-        const int c = GATED ? (tid < 32 ? 64 * group + 2 * tid : 64 + 64 * group + 2 * tid) : 128 * group + 2 * tid;
-        uint32_t two = 0;
-        if (p.bias != nullptr && n0 + c < p.N) two = __ldg(reinterpret_cast<const uint32_t*>(p.bias + n0 + c));
-        *reinterpret_cast<uint32_t*>(&S.bias[buf][c]) = two;
-      }
+      S.bias[buf][bias_col] = next_bias;
+      next_bias = t + pairs < tiles ? load_bias(t + pairs) : 0.f;
+      // Residual chunks are requested one chunk ahead of their use, the first in front of the wait.
+      // (Read and written by the same thread: the residual may be the output.)
+      const bool holds = !SPLIT && group != (int)buf;
+      auto chunk_col = [&](int i) { return 128 * group + (holds && group == 1 ? 32 * (i ^ 2) : 32 * i); };
+      uint4 res[2][4] = {};
+      auto load_residual = [&](int i) {
+        const int c = n0 + chunk_col(i);
+        const uint4* from = reinterpret_cast<const uint4*>(p.residual + row * p.N + c);
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          if (live && c + 8 * g < p.N) res[i & 1][g] = from[g];
+      };
+      if (!GATED && p.residual != nullptr) load_residual(0);
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.acc_full[buf]), (tc >> 1) & 1u, abort_flag, p.status,
                                              0x840 | buf));
       if (!ok) {
@@ -671,7 +685,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
       // The shared columns, the last 64 of buffer 0 (group 1's) and the first 64 of buffer 1
       // (group 0's), leave tensor memory first.  A group without any arrives too: it is
       // done with the last tile.
-      const bool holds = !SPLIT && group != (int)buf;
       uint32_t held[2][32];
       if (holds) {
         const uint32_t shared = buf == 0 ? 192 : 0;
@@ -703,6 +716,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
         others = cluster_addr(mine, cluster_rank() ^ 2u);
       }
       if (GATED) {
+        uint8_t* box = S.stage[warp - 4][boxes & 1u];
         reuse_box();
         uint32_t scales = 0;  // of the row's two blocks
 #pragma unroll
@@ -743,28 +757,25 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
             o.y = mx_cvt4(y[16 * g + 4] * inv, y[16 * g + 5] * inv, y[16 * g + 6] * inv, y[16 * g + 7] * inv);
             o.z = mx_cvt4(y[16 * g + 8] * inv, y[16 * g + 9] * inv, y[16 * g + 10] * inv, y[16 * g + 11] * inv);
             o.w = mx_cvt4(y[16 * g + 12] * inv, y[16 * g + 13] * inv, y[16 * g + 14] * inv, y[16 * g + 15] * inv);
-            *box_chunk<64>(box, lane, 2 * i + g) = o;
+            *box_chunk(box, lane, 2 * i + g) = o;
           }
         }
-        if (row0 < p.M) store_box(&p.tm_out[0], box, (n0 >> 1) + 64 * group, row0);
+        if (row0 < p.M) {
+          store_box(&p.tm_out[0], box, (n0 >> 1) + 64 * group, row0);
+          ++boxes;
+        }
         if (live)
           *reinterpret_cast<uint16_t*>(p.scale + mx_scale_word(row, n, p.q_tile_cols) + 2 * group) = (uint16_t)scales;
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          // 64 columns to a box, the held ones first
-          const int c = 128 * group + (holds && group == 1 ? 32 * (i ^ 2) : 32 * i);
-          if (n0 + (c & ~63) >= p.N) continue;  // (both chunks of a box alike)
+          // 32 columns to a box, the held ones first
+          const int c = chunk_col(i);
+          if (p.residual != nullptr && i < 3) load_residual(i + 1);
+          if (n0 + c >= p.N) continue;
+          uint8_t* box = S.stage[warp - 4][boxes & 1u];
           uint32_t v[32];
           if (!(holds && i < 2)) tmem_ld32(acc + c, v);
-          uint4 res[4] = {};
-          if (p.residual != nullptr && live) {
-            // read and written by the same thread: the residual may be the output
-            const uint4* r = reinterpret_cast<const uint4*>(p.residual + row * p.N + n0 + c);
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-              if (n0 + c + 8 * g < p.N) res[g] = r[g];
-          }
           tmem_wait_ld();
           if (SPLIT) add_others(v, others + 32 * i * 512);
           if (holds && i < 2) {
@@ -780,11 +791,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
 #pragma unroll
             for (int e = 0; e < 32; ++e) y[e] = gelu_tanh(y[e]);
           }
-          if ((i & 1) == 0 && p.tma_out) reuse_box();
+          if (p.tma_out) reuse_box();
           if (p.residual != nullptr) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-              const uint32_t rw[4] = {res[g].x, res[g].y, res[g].z, res[g].w};
+              const uint4 rr = res[i & 1][g];
+              const uint32_t rw[4] = {rr.x, rr.y, rr.z, rr.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const float2 rf = unpack_bf16x2(rw[e]);
@@ -792,7 +804,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
                 y[8 * g + 2 * e + 1] = fmaf(p.alpha, y[8 * g + 2 * e + 1], rf.y);
               }
             }
-          } else {
+          } else if (p.alpha != 1.f) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) y[e] *= p.alpha;
           }
@@ -801,21 +813,23 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
             const uint4 o = make_uint4(pack_bf16x2(y[8 * g], y[8 * g + 1]), pack_bf16x2(y[8 * g + 2], y[8 * g + 3]),
                                        pack_bf16x2(y[8 * g + 4], y[8 * g + 5]), pack_bf16x2(y[8 * g + 6], y[8 * g + 7]));
             if (p.tma_out) {
-              *box_chunk<128>(box, lane, 4 * (i & 1) + g) = o;
+              *box_chunk(box, lane, g) = o;
             } else if (live && n0 + c + 8 * g < p.N) {
               const int col = n0 + c + 8 * g, seg = col / p.n_seg;
               *reinterpret_cast<uint4*>(p.out[seg] + row * p.n_seg + (col - seg * p.n_seg)) = o;
             }
           }
-          if ((i & 1) == 1 && p.tma_out) {
-            // 64 columns are done; rows and columns past the end are not written
-            const int col = n0 + (c & ~63), seg = col / p.n_seg;
-            if (row0 < p.M) store_box(&p.tm_out[seg], box, col - seg * p.n_seg, row0);
+          if (p.tma_out && row0 < p.M) {
+            // rows and columns past the end are not written
+            const int col = n0 + c, seg = p.n_seg == p.N ? 0 : col / p.n_seg;
+            store_box(&p.tm_out[seg], box, col - seg * p.n_seg, row0);
+            ++boxes;
           }
         }
       }
     }
-    reuse_box();  // the TMA has read what it was given
+    if (elect_one_sync()) bulk_wait_read_all();  // the TMA has read what it was given
+    __syncwarp();
   }
 
   tc_fence_before();
@@ -870,17 +884,17 @@ static bool encode_scales(CUtensorMap* m, const void* base, uint64_t rows, uint6
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 2-D map of a row-major result; boxes of 32 rows x 128 bytes of bf16, or 64 bytes of e4m3, swizzled.
+// 2-D map of a row-major result; boxes of 32 rows x 64 bytes, swizzled.
 static bool encode_out(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t bytes) {
   auto fn = mx_encode_fn();
   if (fn == nullptr) return false;
   cuuint64_t dims[2] = {cols, rows};
   cuuint64_t strides[1] = {cols * bytes};
-  cuuint32_t box[2] = {64, 32};
+  cuuint32_t box[2] = {64 / bytes, 32};
   cuuint32_t estr[2] = {1, 1};
   return fn(m, bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            bytes == 1 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -931,9 +945,9 @@ static cudaError_t launch_wide(mx::Params& p, const MxGemmArgs& a, cudaStream_t 
   if (!encode_values(&p.tm_x, a.x, a.M, a.K, 128) || !encode_values(&p.tm_w, a.w, a.N, a.K, 128) ||
       !encode_scales(&p.tm_xs, a.x_scale, a.M, a.K, 1) || !encode_scales(&p.tm_ws, a.w_scale, a.N, a.K, 2))
     return cudaErrorInvalidValue;
-  // The result leaves through 32-row, 64-column boxes, except where a segment
+  // The result leaves through boxes of 32 rows x 64 bytes, except where a segment
   // ends inside of one.
-  p.tma_out = GATED || a.n_out == 1 || p.n_seg % 64 == 0;
+  p.tma_out = GATED || a.n_out == 1 || p.n_seg % 32 == 0;
   for (int i = 0; p.tma_out && i < a.n_out; ++i)
     if (!encode_out(&p.tm_out[i], GATED ? a.q : a.out[i], a.M, p.n_seg, GATED ? 1 : 2)) return cudaErrorInvalidValue;
   p.mt = (int32_t)((a.M + 255) / 256);
