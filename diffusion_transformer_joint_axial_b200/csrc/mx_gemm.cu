@@ -964,27 +964,33 @@ static cudaError_t launch_wide(mx::Params& p, const MxGemmArgs& a, cudaStream_t 
 }
 
 enum class Way { kNarrow, kWide, kSplit };
+static int64_t max64(int64_t a, int64_t b) { return a > b ? a : b; }
 
-// Which kernel for more than one tile of tokens: the estimates, in ns, are a launch plus rounds of
-// tiles over the SMs, with a K step's time in each kernel as measured (B200, us, narrow / pairs /
-// pairs with K split: 512 x 4096 x 4096 16.7 / 17.6 / 15.6, 512 x 4096 x 12288 39 / 38 / 27,
-// 1024 x 4096 x 2048 12.2 / 13.4 / -, 1024 x 4096 x 12288 49 / 42 / -, 2048 x 4096 x 4096 38 / 31 / -; gated
-// 333 x 2048 x 4096 20 / 16 / 13, 1000 x 4096 x 4096 44 / 30 / -).
+// Which kernel for more than one tile of tokens: estimates, in ns, of a launch plus the rounds that the
+// tiles take over the SMs.  A round of the narrow kernel is its K steps and then its epilogue; of
+// the pairs' the longer of the two, as they overlap, except in the first.  The constants are fits to
+// measurements on a B200 (us, narrow / pairs / pairs with K split): 1024 x 4096 x 1024 8.6 / 9.4 / -,
+// 4096 x 12288 x 128 56 / 51 / -, 512 x 4096 x 4096 16.7 / 17.6 / 15, 512 x 4096 x 12288 39 / 38 / 27,
+// 1024 x 4096 x 12288 49 / 42 / -, 2048 x 4096 x 4096 38 / 31 / -, 4096 x 4096 x 256 with a residual 47 / 30 / -;
+// gated 1024 x 2048 x 128 8 / 5.7 / -, 333 x 2048 x 4096 20 / 16 / 13, 1000 x 4096 x 4096 44 / 30 / -.
 static Way choose(const MxGemmArgs& a, int kt, int num_sms) {
   if (a.M <= 128) return Way::kNarrow;
   if (a.M > 128 * 65535ll) return Way::kWide;  // more token tiles than a grid's second axis takes
+  const int64_t act = a.act != QI21_ACT_NONE ? 2400 : 0;
   const mx::Narrow c = a.gated ? narrow_config<true>(a, kt, num_sms) : narrow_config<false>(a, kt, num_sms);
   const int64_t features = a.gated ? 256 : 128;
   const int64_t ctas = ((a.N + features - 1) / features) * ((a.M + 127) / 128) * c.split;
   const bool twos = !a.gated && ctas > num_sms;  // two CTAs to an SM
-  const int64_t per_round = twos ? 2 * num_sms : num_sms;
-  const int64_t narrow = 5000 + (c.split == 1 ? 0 : a.gated ? 6000 : 1500) +
-                         (ctas + per_round - 1) / per_round * ((kt + c.split - 1) / c.split) *
-                             (a.gated ? 700 : twos ? 560 : 370);
-  const int64_t tiles = ((a.M + 255) / 256) * ((a.N + 255) / 256), at_once = num_sms / 2;
-  const int64_t wide = 7500 + (tiles + at_once - 1) / at_once * kt * 345;
+  const int64_t at_once = twos ? 2 * num_sms : num_sms, steps = (kt + c.split - 1) / c.split;
+  const int64_t rounds = (ctas + at_once - 1) / at_once;
+  const int64_t res = a.residual == nullptr ? 0 : rounds > 1 ? 7000 : 3000;
+  const int64_t narrow = 1500 + (c.split == 1 ? 0 : a.gated ? 8000 : 3000) +
+                         rounds * (3900 + act + res + steps * (a.gated ? 500 : twos ? 450 : 352));
+  const int64_t tiles = ((a.M + 255) / 256) * ((a.N + 255) / 256), pairs = num_sms / 2;
+  const int64_t drain = (a.gated ? 2700 : 4400) + act + (a.residual != nullptr ? 2200 : 0);
+  const int64_t wide = 2200 + drain + kt * 360 + ((tiles + pairs - 1) / pairs - 1) * max64(kt * 365 + 600, drain);
   // (of 37 clusters of four CTAs, one CTA to an SM, not all found room at once; 32 did)
-  const int64_t split = 4 * tiles <= num_sms - 20 && kt >= 8 ? 9500 + (kt + 1) / 2 * 345 : INT64_MAX;
+  const int64_t split = 4 * tiles <= num_sms - 20 && kt >= 8 ? 4500 + drain + (kt + 1) / 2 * 360 : INT64_MAX;
   if (split < narrow && split < wide) return Way::kSplit;
   return wide < narrow ? Way::kWide : Way::kNarrow;
 }
