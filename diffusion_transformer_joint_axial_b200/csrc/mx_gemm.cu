@@ -115,7 +115,6 @@ __device__ __forceinline__ float activate(float y, int act) {
 struct __align__(64) Params {
   CUtensorMap tm_x, tm_w, tm_xs, tm_ws;
   CUtensorMap tm_out[kMaxOut];    // pair kernel: 32-row, 64-byte boxes of out[i], or of q
-  int32_t tma_out;                // 1: tm_out is used
   int32_t M, N, K;
   int32_t n_seg;                  // columns per output segment (swiglu: N / 2)
   int32_t kt;                     // K steps of 128
@@ -773,6 +772,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
           const int c = chunk_col(i);
           if (p.residual != nullptr && i < 3) load_residual(i + 1);
           if (n0 + c >= p.N) continue;
+          // (in the last segment the TMA drops what is past N; a box that another segment ends
+          // in is stored by the threads)
+          const int seg = p.n_seg == p.N ? 0 : (n0 + c) / p.n_seg, seg_col = n0 + c - seg * p.n_seg;
+          const bool boxed = seg_col + 32 <= p.n_seg || n0 + c + 32 >= p.N;
           uint8_t* box = S.stage[warp - 4][boxes & 1u];
           uint32_t v[32];
           if (!(holds && i < 2)) tmem_ld32(acc + c, v);
@@ -791,7 +794,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
 #pragma unroll
             for (int e = 0; e < 32; ++e) y[e] = gelu_tanh(y[e]);
           }
-          if (p.tma_out) reuse_box();
+          if (boxed) reuse_box();
           if (p.residual != nullptr) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
@@ -812,17 +815,15 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
           for (int g = 0; g < 4; ++g) {
             const uint4 o = make_uint4(pack_bf16x2(y[8 * g], y[8 * g + 1]), pack_bf16x2(y[8 * g + 2], y[8 * g + 3]),
                                        pack_bf16x2(y[8 * g + 4], y[8 * g + 5]), pack_bf16x2(y[8 * g + 6], y[8 * g + 7]));
-            if (p.tma_out) {
+            if (boxed) {
               *box_chunk(box, lane, g) = o;
             } else if (live && n0 + c + 8 * g < p.N) {
-              const int col = n0 + c + 8 * g, seg = col / p.n_seg;
-              *reinterpret_cast<uint4*>(p.out[seg] + row * p.n_seg + (col - seg * p.n_seg)) = o;
+              const int col = n0 + c + 8 * g, own = col / p.n_seg;
+              *reinterpret_cast<uint4*>(p.out[own] + row * p.n_seg + (col - own * p.n_seg)) = o;
             }
           }
-          if (p.tma_out && row0 < p.M) {
-            // rows and columns past the end are not written
-            const int col = n0 + c, seg = p.n_seg == p.N ? 0 : col / p.n_seg;
-            store_box(&p.tm_out[seg], box, col - seg * p.n_seg, row0);
+          if (boxed && row0 < p.M) {  // (rows past M are not written)
+            store_box(&p.tm_out[seg], box, seg_col, row0);
             ++boxes;
           }
         }
@@ -945,10 +946,7 @@ static cudaError_t launch_wide(mx::Params& p, const MxGemmArgs& a, cudaStream_t 
   if (!encode_values(&p.tm_x, a.x, a.M, a.K, 128) || !encode_values(&p.tm_w, a.w, a.N, a.K, 128) ||
       !encode_scales(&p.tm_xs, a.x_scale, a.M, a.K, 1) || !encode_scales(&p.tm_ws, a.w_scale, a.N, a.K, 2))
     return cudaErrorInvalidValue;
-  // The result leaves through boxes of 32 rows x 64 bytes, except where a segment
-  // ends inside of one.
-  p.tma_out = GATED || a.n_out == 1 || p.n_seg % 32 == 0;
-  for (int i = 0; p.tma_out && i < a.n_out; ++i)
+  for (int i = 0; i < a.n_out; ++i)
     if (!encode_out(&p.tm_out[i], GATED ? a.q : a.out[i], a.M, p.n_seg, GATED ? 1 : 2)) return cudaErrorInvalidValue;
   p.mt = (int32_t)((a.M + 255) / 256);
   p.nt = (int32_t)((a.N + 255) / 256);
