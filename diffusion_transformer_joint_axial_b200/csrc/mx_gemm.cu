@@ -140,14 +140,14 @@ struct __align__(64) Params {
 // the tokens, reading the others' partials in the order of the split.
 //   warp 0     TMA producer
 //   warp 1     TMEM owner and MMA issuer
-//   warps 2-5  epilogue: one feature per thread
+//   warps 2-9  epilogue: one feature per thread, every other sixteen tokens
 //
 // Tensor memory and residency: a CTA waits in its allocation while others of the
 // SM hold the columns, and CTAs of a cluster wait for one another, so an SM must
 // never host CTAs that want more than its 512 columns together.  Shared memory sees to
 // that: at most 256 columns with at least 76 KB (two such CTAs fit), or 512 with more
 // than 151 KB (nothing else fits beside it).
-constexpr int kNarrowThreads = 192;
+constexpr int kNarrowThreads = 320;
 constexpr int kNarrowMaxStages = 8;
 constexpr int kNarrowSlots = 4;
 constexpr int kNarrowMaxSmem = 224 * 1024;
@@ -279,6 +279,7 @@ __global__ void __launch_bounds__(kNarrowThreads) mx_gemm_narrow(const __grid_co
   const int lane = threadIdx.x & 31, quarter = warp & 3;
   const int j = quarter * 32 + lane;  // feature in the block == TMEM lane
   const int f = f0 + j, last = min(c.bn, p.M - m0);
+  const int t0 = warp < 6 ? 0 : 16;  // warps 2-5 and 6-9 take turns
   const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
   bool ok = true;
   if (warp >= 2) {
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(kNarrowThreads) mx_gemm_narrow(const __grid_co
   };
 
   if (c.split == 1) {
-    for (int t = 0; warp >= 2 && ok && t < last; t += 16) {
+    for (int t = t0; warp >= 2 && ok && t < last; t += 32) {
       uint32_t v[16], w[16];
       tmem_ld16(lanes + t, v);
       if (GATED) tmem_ld16(lanes + c.bn + t, w);
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(kNarrowThreads) mx_gemm_narrow(const __grid_co
     }
   } else {
     // partial sums [w][token][feature], over the operands' buffers (all read by now)
-    for (int t = 0; warp >= 2 && t < last; t += 16) {
+    for (int t = t0; warp >= 2 && t < last; t += 32) {
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
         uint32_t v[16];
@@ -381,7 +382,7 @@ __global__ void __launch_bounds__(kNarrowThreads) mx_gemm_narrow(const __grid_co
     }
     cluster_sync_all();
     const int share = (last + c.split - 1) / c.split, end = min(last, (rank + 1) * share);
-    for (int t = rank * share; warp >= 2 && ok && t < end; t += 16) {
+    for (int t = rank * share + t0; warp >= 2 && ok && t < end; t += 32) {
       const int n = min(16, end - t);
       float y[16] = {}, u[16] = {};
       for (int r = 0; r < c.split; ++r) {
@@ -899,6 +900,9 @@ static bool encode_out(CUtensorMap* m, const void* base, uint64_t rows, uint64_t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// What splitting K costs in the narrow kernel, ns.
+static int64_t split_cost(int blocks, int bn) { return 1500 + bn * (blocks == 2 ? 48 : 12); }
+
 // Tokens per tile, stages, TMEM columns and the split of K for few tokens.
 template <bool GATED>
 static mx::Narrow narrow_config(const MxGemmArgs& a, int kt, int num_sms) {
@@ -909,14 +913,21 @@ static mx::Narrow narrow_config(const MxGemmArgs& a, int kt, int num_sms) {
   c.cols = cols <= 256 ? 256 : 512;
   const int stage = NW * (mx::kW + mx::kTileBytes) + c.bn * mx::BK + mx::kTileBytes;
   const int64_t tiles = ((a.N + NW * 128 - 1) / (NW * 128)) * ((a.M + c.bn - 1) / c.bn);
-  // Splitting K costs 1.4 us of cluster barriers and remote reads, and pays only while SMs would
-  // idle (measured: 16 x 4096 x 4096, 32 tiles: 13.8 us whole, 8.6 in 4 parts; 96 tiles in 2 parts:
-  // 18 -> 21 us; 128 x 4096 x 1024, 8 steps: 7.6 -> 10.4 us).  One CTA per SM takes all of its shared memory for stages
+  // Parts of K: a step takes 310 ns; splitting costs barriers and remote reads, more with more
+  // tokens, and pays only while SMs would idle (us in 1 / 2 / 4 / 8 parts: 16 x 4096 x 4096, 32 tiles,
+  // 12.7 / 9.2 / 8.0 / 9.8; 1 x 320 x 1568 6.4 / 5.8 / 5.6 / 6.9; 75 x 184 x 7456 22 / 15 / 10.5 / 11.3;
+  // 128 x 4096 x 1024 7.6 / 10.4).  Of 37 clusters of 4 CTAs, one to an SM, not all found room on
+  // the GPCs at once; 32 did.  One CTA per SM takes all of its shared memory for stages
   // (77 x 12288 x 4096 gated: 34 us with half, 25 with all); more tiles than SMs run in twos.
-  // Clusters of 8 such CTAs find room on the GPCs only while few are wanted (256 x 1024 x 4096, 16 tiles:
-  // 24 us in 8 parts; 512 x 1024, 32 tiles: 13 us in 4).
   c.split = 1;
-  while (c.split < 8 && tiles * c.split * 2 <= (c.split == 4 ? 64 : num_sms) && kt >= 16 * c.split) c.split *= 2;
+  int64_t best = (int64_t)kt * 310;
+  for (int s = 2; s <= 4 && tiles * s <= (s == 4 ? num_sms - 20 : num_sms) && s <= kt; s *= 2) {
+    const int64_t cost = (int64_t)((kt + s - 1) / s) * 310 + split_cost(NW, c.bn);
+    if (cost < best) {
+      best = cost;
+      c.split = s;
+    }
+  }
   const int room = (c.cols == 256 && tiles * c.split > num_sms ? 110 : 220) * 1024;
   c.stages = room / stage < mx::kNarrowMaxStages ? room / stage : mx::kNarrowMaxStages;
   const int least = (c.cols == 256 ? 76 : 152) * 1024;
@@ -982,7 +993,7 @@ static Way choose(const MxGemmArgs& a, int kt, int num_sms) {
   const int64_t at_once = twos ? 2 * num_sms : num_sms, steps = (kt + c.split - 1) / c.split;
   const int64_t rounds = (ctas + at_once - 1) / at_once;
   const int64_t res = a.residual == nullptr ? 0 : rounds > 1 ? 7000 : 3000;
-  const int64_t narrow = 1500 + (c.split == 1 ? 0 : a.gated ? 8000 : 3000) +
+  const int64_t narrow = 1500 + (c.split == 1 ? 0 : split_cost(a.gated ? 2 : 1, c.bn)) +
                          rounds * (3900 + act + res + steps * (a.gated ? 500 : twos ? 450 : 352));
   const int64_t tiles = ((a.M + 255) / 256) * ((a.N + 255) / 256), pairs = num_sms / 2;
   const int64_t drain = (a.gated ? 2700 : 4400) + act + (a.residual != nullptr ? 2200 : 0);
