@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(int64_t groups, int32_
 template <int TR, int C, bool ADD>
 __global__ void __launch_bounds__(256) rmsnorm_mx_kernel(int64_t M, int32_t D, int32_t tile_cols,
                                                          const __nv_bfloat16* x, const __nv_bfloat16* delta,
-                                                         const __nv_bfloat16* __restrict__ w, float eps,
+                                                         const __nv_bfloat16* __restrict__ w, float inv_d, float eps,
                                                          __nv_bfloat16* sum, uint8_t* __restrict__ q,
                                                          uint8_t* __restrict__ scale) {
   constexpr int kWarps = TR / 32, kKept = C > 0 ? C : 1;
@@ -182,11 +182,11 @@ __global__ void __launch_bounds__(256) rmsnorm_mx_kernel(int64_t M, int32_t D, i
   if (kWarps > 1) {
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = all;
     __syncthreads();
-    all = 0.f;
+    all = part[threadIdx.x / TR * kWarps + (threadIdx.x & (kWarps - 1))];
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) all += part[threadIdx.x / TR * kWarps + i];
+    for (int o = kWarps / 2; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
   }
-  const float rs = 1.f / sqrtf(all / static_cast<float>(D) + eps);
+  const float rs = rsqrtf(fmaf(all, inv_d, eps));
 
   if (C > 0) {
 #pragma unroll
@@ -214,7 +214,7 @@ cudaError_t run_rmsnorm_mx(int64_t M, int32_t D, const void* x, const void* delt
   return launch_dependent(delta != nullptr ? rmsnorm_mx_kernel<TR, C, true> : rmsnorm_mx_kernel<TR, C, false>,
                           dim3((unsigned)((M + kRows - 1) / kRows)), 256, 0, 1, stream, M, D, (D + 127) / 128,
                           static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(delta),
-                          static_cast<const __nv_bfloat16*>(w), eps, static_cast<__nv_bfloat16*>(sum),
+                          static_cast<const __nv_bfloat16*>(w), 1.f / static_cast<float>(D), eps, static_cast<__nv_bfloat16*>(sum),
                           static_cast<uint8_t*>(q), static_cast<uint8_t*>(scale));
 }
 

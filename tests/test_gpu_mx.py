@@ -125,7 +125,8 @@ def test_rmsnorm_mx(cuda_device, M, D, delta):
         got = qi.rmsnorm_mx(x.to(dev), w.to(dev), eps)
     y = X.rms_norm(W.as_f64(x), W.as_f64(w), eps)
     # fp32 sum of D squares over at least 32 partial sums: D / 32 + 8 roundings of 2^-24 at
-    # most, halved by the root; six more for mean, root, quotient and the two products
+    # most, and two for the mean, all halved by the root; four for the reciprocal root (two units
+    # in the last place), one for the product with it (h * w is exact)
     _check_rounded(got, y, (D / 64 + 10) * 2.0 ** -24)
 
 
