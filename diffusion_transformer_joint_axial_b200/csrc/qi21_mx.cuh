@@ -11,7 +11,7 @@
 
 #include <atomic>
 
-#include "qi21_device.cuh"
+#include "qi21_cluster.cuh"
 
 namespace qi21 {
 
