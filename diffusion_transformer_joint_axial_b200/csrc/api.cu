@@ -610,9 +610,10 @@ size_t qi21_mx_scale_size(int64_t rows, int64_t K) {
 
 // Sizes and buffers of an MX matrix.
 static qi21_status check_mx_dims(int64_t rows, int64_t K, const char* name) {
-  if (rows < 0 || K < 32 || K % 32 != 0 || rows > INT32_MAX || K > INT32_MAX - 127)
-    return fail(QI21_ERR_INVALID_ARG, "%s: rows must be >= 0 and the length a multiple of 32, >= 32 (got %lld x %lld)",
-                name, (long long)rows, (long long)K);
+  if (rows < 0 || K < 32 || K % 32 != 0 || rows > INT32_MAX || K > 1 << 24)
+    return fail(QI21_ERR_INVALID_ARG,
+                "%s: rows must be in [0, 2^31) and the length a multiple of 32 in [32, 2^24] (got %lld x %lld)", name,
+                (long long)rows, (long long)K);
   return QI21_OK;
 }
 

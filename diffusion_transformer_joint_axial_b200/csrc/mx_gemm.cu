@@ -495,7 +495,6 @@ __device__ __forceinline__ void reuse_box() {
   __syncwarp();
 }
 
-//
 // SPLIT: one tile to a cluster of two pairs, each with half of K, for calls with few tiles.  When
 // both are done, the pairs swap halves of the tile's columns through shared
 // memory (fp32, [column][token]): pair i finishes what group i of its epilogue warps
@@ -611,7 +610,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
             copy_scales_pair(sw + 4, wsd + (kTileBytes >> 4));
             const int blocks = (p.K - kb * BK) >> 5;  // the blocks past K hold nothing
             if (blocks >= 4) {
-  #pragma unroll
+#pragma unroll
               for (int b = 0; b < 4; ++b)
                 mma_scaled_pair(acc, xd + 2 * b, wd + 2 * b, idesc(256, 256) | idesc_block(b), sx, sw, kb > k_begin || b > 0);
             } else {
@@ -776,7 +775,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
           // (in the last segment the TMA drops what is past N; a box that another segment ends
           // in is stored by the threads)
           const int seg = p.n_seg == p.N ? 0 : (n0 + c) / p.n_seg, seg_col = n0 + c - seg * p.n_seg;
-          const bool boxed = seg_col + 32 <= p.n_seg || n0 + c + 32 >= p.N;
+          const bool boxed = seg_col + 32 <= p.n_seg || n0 + c - seg_col + p.n_seg == p.N;
           uint8_t* box = S.stage[warp - 4][boxes & 1u];
           uint32_t v[32];
           if (!(holds && i < 2)) tmem_ld32(acc + c, v);

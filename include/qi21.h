@@ -329,7 +329,7 @@ qi21_status qi21_swiglu(int64_t n, const void* g, const void* u, void* m, void* 
  * Block-scaled 8-bit (MX) forms of the block's row-wise and projection steps: twice
  * the tensor rate of bf16 and half the bytes of every weight.
  *
- * An MX matrix [R, K] (K a multiple of 32) is two device buffers.  Values: e4m3
+ * An MX matrix [R, K] (K a multiple of 32, at most 2^24) is two device buffers.  Values: e4m3
  * bytes, row-major.  Scales: one e8m0 byte (exponent + 127) per 32 consecutive
  * values of a row, in tiles of 128 rows x 4 blocks of 512 bytes, tile (r / 128,
  * b / 4) at index (r / 128) * ceil(K / 128) + b / 4, the byte of row r and block b
@@ -378,7 +378,7 @@ typedef enum {
  * (n_out segments as in qi21_linear), the down projection and the Euler step
  * (residual, alpha), and the two-layer MLPs of the text and time embeddings (act).
  * From one row (a time embedding) to every token of a request.
- *   x, x_scale  MX [M, K]; w, w_scale  MX [N, K]; K a multiple of 32, >= 32.
+ *   x, x_scale  MX [M, K]; w, w_scale  MX [N, K].  Outputs overlap no input but the residual.
  *   bias        device bf16 [N] or NULL.
  *   act         qi21_activation.
  *   residual    device bf16 [M, N] or NULL (n_out = 1 with it); may be out[0].

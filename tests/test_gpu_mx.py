@@ -269,6 +269,44 @@ def test_exact_products_read_every_scale(cuda_device):
         assert torch.equal(got.cpu(), want), (M, N, K)
 
 
+def test_more_token_tiles_than_a_grid_axis(cuda_device):
+    """Eight million rows into four segments of eight columns: one 64-byte box holds them all.  The rows repeat, so
+    the result of the first 1024, checked on their own, must repeat too."""
+    rng = np.random.default_rng(14)
+    M, K, N = 128 * 65535 + 1, 32, 32
+    x, xv = _mx_operand(rng, 1024, K, 1.0, cuda_device)
+    w, wv = _mx_operand(rng, N, K, K ** -0.5, cuda_device)
+    few = qi.linear_mx(x, w, n_out=4)
+    _check_linear(few, xv, wv, None, "none", None, 1.0, K)
+    q = x.q.view(torch.uint8).repeat(8193, 1)[:M].contiguous().view(torch.float8_e4m3fn)
+    scale = x.scale.view(torch.uint8).repeat(8192, 1, 1, 1, 1).view(torch.float8_e8m0fnu)
+    outs = qi.linear_mx(qi.MXTensor(q, scale), w, n_out=4)
+    for o, f in zip(outs, few):
+        whole = (M // 1024) * 1024
+        assert bool((o[:whole].view(-1, 1024, 8) == f).all()) and torch.equal(o[whole:], f[: M - whole])
+
+
+@pytest.mark.parametrize("M", [40, 300, 1100])
+def test_products_leave_what_lies_behind_alone(cuda_device, M):
+    """Rows behind the last token, in values and scales, stay as they were."""
+    rng = np.random.default_rng(M)
+    dev, K, N = cuda_device, 512, 4096
+    x, _ = _mx_operand(rng, M, K, 1.0, dev)
+    w, _ = _mx_operand(rng, N, K, K ** -0.5, dev)
+    out = torch.full((M + 5, N), 7.0, dtype=BF, device=dev)
+    qi.linear_mx(x, w, out=[out[:M]])
+    assert bool((out[M:] == 7).all()) and not bool((out[:M] == 7).all(1).any())
+    q = torch.full((M + 5, N // 2), 9, dtype=torch.uint8, device=dev)
+    groups = (M + 127) // 128
+    scale = torch.full((groups, N // 256, 32, 4, 4), 0xAB, dtype=torch.uint8, device=dev)
+    qi.linear_swiglu_mx(x, w, out=qi.MXTensor(q[:M].view(torch.float8_e4m3fn), scale.view(torch.float8_e8m0fnu)))
+    assert bool((q[M:] == 9).all())
+    s = scale.cpu().numpy()
+    r, b = np.arange(groups * 128)[:, None], np.arange(N // 64)[None, :]
+    full = s[r // 128, b // 4, r % 32, r % 128 // 32, b % 4]
+    assert (full[M:] == 0xAB).all() and (full[:M] != 0xAB).all()
+
+
 def test_linear_mx_residual_in_place(cuda_device):
     rng = np.random.default_rng(12)
     for M, N, K in ((40, 264, 256), (900, 512, 256)):

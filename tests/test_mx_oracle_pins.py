@@ -94,7 +94,7 @@ def test_scale_size(lib):
 
 def test_quantize_rejects(lib):
     f = lambda M=4, K=64, x=16, q=16, s=16: lib.qi21_mx_quantize(M, K, p(x), p(q), p(s), None)
-    assert f(K=48) == BAD and f(K=0) == BAD and f(M=-1) == BAD and f(M=1 << 31) == BAD
+    assert f(K=48) == BAD and f(K=0) == BAD and f(M=-1) == BAD and f(M=1 << 31) == BAD and f(K=(1 << 24) + 32) == BAD
     assert f(x=0) == BAD and f(q=24) == BAD and f(s=20) == BAD
     assert f(M=0, x=0) == qb.QI21_OK
 
