@@ -141,6 +141,9 @@ struct __align__(64) Params {
 //   warp 0     TMA producer
 //   warp 1     TMEM owner and MMA issuer
 //   warps 2-9  epilogue: one feature per thread, every other sixteen tokens
+// Measured on a B200: 1 x 24576 x 4096 in 20.5 us (5.1 TB/s with launch and ramp), 16 x 4096 x 4096
+// in 7.5, 77 x 12288 x 4096 gated in 24 (4.3 TB/s), 1 x 4096 x 256 in 3.2.  Bound by HBM for few tokens, by
+// what an SM takes from L2 (64 bytes a cycle) for many.
 //
 // Tensor memory and residency: a CTA waits in its allocation while others of the
 // SM hold the columns, and CTAs of a cluster wait for one another, so an SM must
@@ -422,6 +425,11 @@ __global__ void __launch_bounds__(kNarrowThreads) mx_gemm_narrow(const __grid_co
 // and [192, 448), and the scales of four K steps behind them.  The epilogue drains the
 // shared columns first and then lets the next tile's MMAs start, so only that
 // part of an epilogue is not hidden.
+// Measured on a B200: 4096 x 12288 x 4096 in 150 us, 2.75 PFLOP/s, the tensor pipe busy 73 % of
+// the cycles; gated 4096 x 24576 x 4096 in 288 us, 2.86 PFLOP/s, 80 %; 16384 rows of it in 1.25 ms
+// under the power cap.  Bound by the tensor pipe and the shared memory that it and the TMA share: a
+// stage's MMAs take 512 cycles alone, about 600 beside the loads (the same with 4, 5 and 6 stages; with
+// stages of K = 256; without the scale copies).
 constexpr int kWideThreads = 384;
 constexpr int kWideStages = 5;
 constexpr int kGroup = 16;
