@@ -498,6 +498,7 @@ MX_ACTIVATIONS = {"none": 0, "silu": 1, "gelu_tanh": 2, "gelu": 2}
 
 _mx_lib = None
 _E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+_ONE = _vp * 1
 
 
 def _mx_start(t, name):
@@ -520,6 +521,11 @@ def _mx_call(device, fn, *args):
             status = fn(*args, torch._C._cuda_getCurrentRawStream(i))
     if status != QI21_OK:
         _check(status)
+
+
+def _like(shape, last):
+    """``shape`` with another last dimension."""
+    return (shape[0], last) if len(shape) == 2 else shape[:-1] + (last,)
 
 
 def _rows(shape):
@@ -630,22 +636,24 @@ def linear_mx(x, w, bias=None, n_out=1, act="none", residual=None, alpha=1.0, ou
         raise QI21Error(QI21_ERR_INVALID_ARG, "unknown activation %r" % (act,))
     if n_out < 1 or N % n_out != 0:
         raise QI21Error(QI21_ERR_INVALID_ARG, "N=%d does not split into %d segments" % (N, n_out))
-    lead = shape[:-1]
     if residual is not None:
-        _need(residual, "residual", lead + (N,), torch.bfloat16, dev)
-    seg = lead + (N // n_out,)
+        _need(residual, "residual", _like(shape, N), torch.bfloat16, dev)
+    seg = _like(shape, N // n_out)
     if out is None:
         out = [torch.empty(seg, dtype=torch.bfloat16, device=dev) for _ in range(n_out)]
     if len(out) != n_out:
         raise QI21Error(QI21_ERR_INVALID_ARG, "need %d output tensors" % n_out)
     for o in out:
         _need(o, "out[i]", seg, torch.bfloat16, dev)
+    outs = _ONE(out[0].data_ptr()) if n_out == 1 else (_vp * n_out)(*[o.data_ptr() for o in out])
     if workspace is None:
         workspace = new_workspace(WORKSPACE_HEADER_BYTES, dev)
+    elif workspace.device != dev:
+        raise QI21Error(QI21_ERR_INVALID_ARG, "workspace must be on %s" % dev)
     _mx_call(dev, L_.qi21_linear_mx, R, N, K, xq.data_ptr(), x.scale.data_ptr(), wq.data_ptr(),
              w.scale.data_ptr(), None if bias is None else bias.data_ptr(), MX_ACTIVATIONS[act],
              None if residual is None else residual.data_ptr(), alpha,
-             (_vp * n_out)(*[o.data_ptr() for o in out]), n_out, workspace.data_ptr(), workspace.nbytes)
+             outs, n_out, workspace.data_ptr(), workspace.nbytes)
     return out
 
 
@@ -665,12 +673,14 @@ def linear_swiglu_mx(x, w_il, bias_il=None, out=None, workspace=None):
         raise QI21Error(QI21_ERR_INVALID_ARG, "the gate and up rows must come in blocks of 128 (N=%d)" % N)
     if bias_il is not None:
         _need(bias_il, "bias", (N,), torch.bfloat16, dev)
-    hidden = shape[:-1] + (N // 2,)
+    hidden = _like(shape, N // 2)
     if out is None:
         out = mx_empty(hidden, dev)
     _need_mx(out, "out", hidden, R, dev)
     if workspace is None:
         workspace = new_workspace(WORKSPACE_HEADER_BYTES, dev)
+    elif workspace.device != dev:
+        raise QI21Error(QI21_ERR_INVALID_ARG, "workspace must be on %s" % dev)
     _mx_call(dev, L_.qi21_linear_swiglu_mx, R, N, K, xq.data_ptr(), x.scale.data_ptr(), wq.data_ptr(),
              w_il.scale.data_ptr(), None if bias_il is None else bias_il.data_ptr(), out.q.data_ptr(),
              out.scale.data_ptr(), workspace.data_ptr(), workspace.nbytes)

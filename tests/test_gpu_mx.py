@@ -453,6 +453,10 @@ def test_binding_refuses(cuda_device):
            lambda: qi.linear_mx(mx, w, alpha=float("nan")),
            lambda: qi.linear_mx(qi.MXTensor(mx.q, mx.scale.view(torch.uint8)), w),
            lambda: qi.linear_mx(mx, w, workspace=torch.zeros(100, dtype=torch.uint8, device=dev)),
+           lambda: qi.linear_mx(mx, w, workspace=torch.zeros(256, dtype=torch.uint8)),
+           lambda: qi.linear_swiglu_mx(mx, w, workspace=torch.zeros(256, dtype=torch.uint8)),
+           lambda: qi.mx_quantize(x.cpu()), lambda: qi.linear_mx(qi.mx_empty((4, 64), "cpu"), w),
+           lambda: qi.linear_mx(mx, qi.mx_empty((256, 64), "cpu")),
            lambda: qi.linear_swiglu_mx(mx, qi.mx_empty((128, 64), dev)),
            lambda: qi.linear_swiglu_mx(mx, w, out=qi.mx_empty((4, 256), dev))]
     for i, call in enumerate(bad):
