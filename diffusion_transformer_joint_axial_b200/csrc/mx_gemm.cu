@@ -115,6 +115,7 @@ __device__ __forceinline__ float activate(float y, int act) {
 struct __align__(64) Params {
   CUtensorMap tm_x, tm_w, tm_xs, tm_ws;
   CUtensorMap tm_out[kMaxOut];    // pair kernel: 32-row, 64-byte boxes of out[i], or of q
+  CUtensorMap tm_res;             // ... and of the residual
   int32_t M, N, K;
   int32_t n_seg;                  // columns per output segment (swiglu: N / 2)
   int32_t kt;                     // K steps of 128
@@ -438,16 +439,18 @@ constexpr int kWideStageBytes = 2 * kOperand + 3 * kTileBytes;
 constexpr uint32_t kAccShift = 192;
 constexpr uint32_t kWideScaleCol = 448;
 constexpr uint32_t kSlots = 4;  // of 4 (X) + 8 (W) scale columns each
+constexpr int kBoxes = 3;
 
 struct __align__(1024) WideSmem {
   uint8_t x[kWideStages][kOperand];
   uint8_t w[kWideStages][kOperand];
-  uint8_t stage[8][2][32 * 64];      // two boxes per epilogue warp (swizzled: 512-byte aligned)
+  uint8_t stage[8][kBoxes][32 * 64];  // boxes of each epilogue warp (swizzled: 512-byte aligned)
   uint8_t ws[kWideStages][2 * kTileBytes];
   uint8_t xs[kWideStages][kTileBytes];
   float bias[2][256];                // of this tile and the next
   uint64_t full[kWideStages], empty[kWideStages];
   uint64_t acc_full[2], acc_free, drain;
+  uint64_t res_full[8][kBoxes];
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -496,13 +499,16 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, uint8_t* box, 
     bulk_commit_group();
   }
 }
-// A warp has two boxes and uses them in turn: the one before the last store's may be
-// written again once the TMA has read it.
+// A warp uses its boxes in turn: the one that comes may be written once the TMA has
+// read it, that is when at most the last two stores are not.
 __device__ __forceinline__ void reuse_box() {
-  if (elect_one_sync()) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+  if (elect_one_sync()) asm volatile("cp.async.bulk.wait_group.read 2;" ::: "memory");
   __syncwarp();
 }
 
+// A residual comes the same way: the TMA loads the chunk into the box that its result will leave from,
+// one chunk ahead.  (Loads by the threads, 16 bytes of 32 rows each, cost 2.5 us a tile in the L1
+// cache: 4096 x 4096 x 256 took 31 us with a residual, 21 without.)
 // SPLIT: one tile to a cluster of two pairs, each with half of K, for calls with few tiles.  When
 // both are done, the pairs swap halves of the tile's columns through shared
 // memory (fp32, [column][token]): pair i finishes what group i of its epilogue warps
@@ -526,6 +532,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
     mbar_init(smem_u32(&S.acc_full[1]), 1);
     mbar_init(smem_u32(&S.acc_free), 16);  // one arrival per epilogue warp of the pair
     mbar_init(smem_u32(&S.drain), 1);
+    for (int i = 0; i < 8 * kBoxes; ++i) mbar_init(smem_u32(&S.res_full[0][i]), 1);
     S.abort_flag = 0;
     fence_mbar_init();
   }
@@ -647,7 +654,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t free_bar = cluster_addr(smem_u32(&S.acc_free), first);
     const int tid = threadIdx.x & 127, lane = threadIdx.x & 31;
-    uint32_t boxes = 0;  // stored so far
+    uint32_t slot = 0, turn = 0;  // the box that comes, and the parity of its use
+    bool coming = false;          // its residual is requested
     uint32_t tc = 0;
     bool ok = true;
     // Each thread brings one of its group's 128 biases a tile, requested a tile ahead.
@@ -668,19 +676,26 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
       const bool live = row < p.M;
       S.bias[buf][bias_col] = next_bias;
       next_bias = t + pairs < tiles ? load_bias(t + pairs) : 0.f;
-      // Residual chunks are requested one chunk ahead of their use, the first in front of the wait.
-      // (Read and written by the same thread: the residual may be the output.)
       const bool holds = !SPLIT && group != (int)buf;
+      // plain: the columns of chunk i, the held ones first, and the next chunk that N reaches
       auto chunk_col = [&](int i) { return 128 * group + (holds && group == 1 ? 32 * (i ^ 2) : 32 * i); };
-      uint4 res[2][4] = {};
-      auto load_residual = [&](int i) {
-        const int c = n0 + chunk_col(i);
-        const uint4* from = reinterpret_cast<const uint4*>(p.residual + row * p.N + c);
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          if (live && c + 8 * g < p.N) res[i & 1][g] = from[g];
+      const bool add = !GATED && p.residual != nullptr && row0 < p.M && !(SPLIT && group != part);
+      auto request = [&](int from, uint32_t box) {
+        for (int i = from; i < 4; ++i)
+          if (n0 + chunk_col(i) < p.N) {
+            if (elect_one_sync()) {
+              // the box's last store has been read: only the last one of all may not be
+              asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+              const uint32_t bar = smem_u32(&S.res_full[warp - 4][box]);
+              mbar_arrive_expect_tx(bar, 32 * 64);
+              tma_load_2d(smem_u32(S.stage[warp - 4][box]), &p.tm_res, bar, n0 + chunk_col(i), row0);
+            }
+            __syncwarp();
+            return true;
+          }
+        return false;
       };
-      if (!GATED && p.residual != nullptr) load_residual(0);
+      if (add) coming = request(0, slot);
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.acc_full[buf]), (tc >> 1) & 1u, abort_flag, p.status,
                                              0x840 | buf));
       if (!ok) {
@@ -723,7 +738,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
         others = cluster_addr(mine, cluster_rank() ^ 2u);
       }
       if (GATED) {
-        uint8_t* box = S.stage[warp - 4][boxes & 1u];
+        uint8_t* box = S.stage[warp - 4][slot];
         reuse_box();
         uint32_t scales = 0;  // of the row's two blocks
 #pragma unroll
@@ -769,7 +784,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
         }
         if (row0 < p.M) {
           store_box(&p.tm_out[0], box, (n0 >> 1) + 64 * group, row0);
-          ++boxes;
+          if (++slot == kBoxes) slot = 0, turn ^= 1u;
         }
         if (live)
           *reinterpret_cast<uint16_t*>(p.scale + mx_scale_word(row, n, p.q_tile_cols) + 2 * group) = (uint16_t)scales;
@@ -778,13 +793,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
         for (int i = 0; i < 4; ++i) {
           // 32 columns to a box, the held ones first
           const int c = chunk_col(i);
-          if (p.residual != nullptr && i < 3) load_residual(i + 1);
           if (n0 + c >= p.N) continue;
           // (in the last segment the TMA drops what is past N; a box that another segment ends
           // in is stored by the threads)
           const int seg = p.n_seg == p.N ? 0 : (n0 + c) / p.n_seg, seg_col = n0 + c - seg * p.n_seg;
           const bool boxed = seg_col + 32 <= p.n_seg || n0 + c - seg_col + p.n_seg == p.N;
-          uint8_t* box = S.stage[warp - 4][boxes & 1u];
+          uint8_t* box = S.stage[warp - 4][slot];
+          const bool more = add && request(i + 1, slot + 1 == kBoxes ? 0 : slot + 1);
           uint32_t v[32];
           if (!(holds && i < 2)) tmem_ld32(acc + c, v);
           tmem_wait_ld();
@@ -802,11 +817,18 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
 #pragma unroll
             for (int e = 0; e < 32; ++e) y[e] = gelu_tanh(y[e]);
           }
-          if (boxed) reuse_box();
-          if (p.residual != nullptr) {
+          if (add) {
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.res_full[warp - 4][slot]), turn, abort_flag, p.status,
+                                                   0x850));
+            if (!ok) {
+              const uint32_t next = slot + 1 == kBoxes ? 0 : slot + 1;
+              if (more) mbar_wait(smem_u32(&S.res_full[warp - 4][next]), next == 0 ? turn ^ 1u : turn, nullptr, nullptr, 0);
+              break;
+            }
+            coming = more;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-              const uint4 rr = res[i & 1][g];
+              const uint4 rr = *box_chunk(box, lane, g);
               const uint32_t rw[4] = {rr.x, rr.y, rr.z, rr.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -815,9 +837,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
                 y[8 * g + 2 * e + 1] = fmaf(p.alpha, y[8 * g + 2 * e + 1], rf.y);
               }
             }
-          } else if (p.alpha != 1.f) {
+          } else {
+            if (boxed) reuse_box();
+            if (p.alpha != 1.f) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] *= p.alpha;
+              for (int e = 0; e < 32; ++e) y[e] *= p.alpha;
+            }
           }
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
@@ -832,11 +857,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
           }
           if (boxed && row0 < p.M) {  // (rows past M are not written)
             store_box(&p.tm_out[seg], box, seg_col, row0);
-            ++boxes;
+            if (++slot == kBoxes) slot = 0, turn ^= 1u;
           }
         }
       }
     }
+    // (a request that a broken wait left behind lands before the CTA may exit)
+    if (coming) mbar_wait(smem_u32(&S.res_full[warp - 4][slot]), turn, nullptr, nullptr, 0);
     if (elect_one_sync()) bulk_wait_read_all();  // the TMA has read what it was given
     __syncwarp();
   }
@@ -964,6 +991,7 @@ static cudaError_t launch_wide(mx::Params& p, const MxGemmArgs& a, cudaStream_t 
   if (!encode_values(&p.tm_x, a.x, a.M, a.K, 128) || !encode_values(&p.tm_w, a.w, a.N, a.K, 128) ||
       !encode_scales(&p.tm_xs, a.x_scale, a.M, a.K, 1) || !encode_scales(&p.tm_ws, a.w_scale, a.N, a.K, 2))
     return cudaErrorInvalidValue;
+  if (a.residual != nullptr && !encode_out(&p.tm_res, a.residual, a.M, a.N, 2)) return cudaErrorInvalidValue;
   for (int i = 0; i < a.n_out; ++i)
     if (!encode_out(&p.tm_out[i], GATED ? a.q : a.out[i], a.M, p.n_seg, GATED ? 1 : 2)) return cudaErrorInvalidValue;
   p.mt = (int32_t)((a.M + 255) / 256);
@@ -987,7 +1015,7 @@ static int64_t max64(int64_t a, int64_t b) { return a > b ? a : b; }
 // the pairs' the longer of the two, as they overlap, except in the first.  The constants are fits to
 // measurements on a B200 (us, narrow / pairs / pairs with K split): 1024 x 4096 x 1024 8.6 / 9.4 / -,
 // 4096 x 12288 x 128 56 / 51 / -, 512 x 4096 x 4096 16.7 / 17.6 / 15, 512 x 4096 x 12288 39 / 38 / 27,
-// 1024 x 4096 x 12288 49 / 42 / -, 2048 x 4096 x 4096 38 / 31 / -, 4096 x 4096 x 256 with a residual 47 / 30 / -;
+// 1024 x 4096 x 12288 49 / 42 / -, 2048 x 4096 x 4096 38 / 31 / -, 4096 x 4096 x 256 with a residual 47 / 25 / -;
 // gated 1024 x 2048 x 128 8 / 5.7 / -, 333 x 2048 x 4096 20 / 16 / 13, 1000 x 4096 x 4096 44 / 30 / -.
 static Way choose(const MxGemmArgs& a, int kt, int num_sms) {
   if (a.M <= 128) return Way::kNarrow;
@@ -1003,7 +1031,7 @@ static Way choose(const MxGemmArgs& a, int kt, int num_sms) {
   const int64_t narrow = 1500 + (c.split == 1 ? 0 : split_cost(a.gated ? 2 : 1, c.bn)) +
                          rounds * (3900 + act + res + steps * (a.gated ? 500 : twos ? 450 : 352));
   const int64_t tiles = ((a.M + 255) / 256) * ((a.N + 255) / 256), pairs = num_sms / 2;
-  const int64_t drain = (a.gated ? 2700 : 4400) + act + (a.residual != nullptr ? 2200 : 0);
+  const int64_t drain = (a.gated ? 2700 : 4400) + act + (a.residual != nullptr ? 1000 : 0);
   const int64_t wide = 2200 + drain + kt * 360 + ((tiles + pairs - 1) / pairs - 1) * max64(kt * 365 + 600, drain);
   // (of 37 clusters of four CTAs, one CTA to an SM, not all found room at once; 32 did)
   const int64_t split = 4 * tiles <= num_sms - 20 && kt >= 8 ? 4500 + drain + (kt + 1) / 2 * 360 : INT64_MAX;

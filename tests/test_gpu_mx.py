@@ -309,7 +309,7 @@ def test_products_leave_what_lies_behind_alone(cuda_device, M):
 
 def test_linear_mx_residual_in_place(cuda_device):
     rng = np.random.default_rng(12)
-    for M, N, K in ((40, 264, 256), (900, 512, 256)):
+    for M, N, K in ((40, 264, 256), (900, 512, 256), (400, 4104, 4096), (3000, 2056, 512), (5000, 4096, 320)):
         x, _ = _mx_operand(rng, M, K, 1.0, cuda_device)
         w, _ = _mx_operand(rng, N, K, K ** -0.5, cuda_device)
         r = _bf(rng.standard_normal((M, N))).to(cuda_device)
