@@ -2,7 +2,7 @@
 // the residual's addition in front of it.  Both are bound by memory: each
 // value is read once in bf16 and written once in 8 bits.  Measured on a B200 whose
 // copies run at 6.55 TB/s: quantising 28160 x 4096 takes 54 us (6.5 TB/s), the norm of
-// 28160 x 4096 with the addition 118 us (6.9 TB/s, reads and writes mixed 1 : 0.75); without it 66 us
+// 28160 x 4096 with the addition 119 us (6.8 TB/s, reads and writes mixed 1 : 0.75); without it 65 us
 // (5.3 TB/s), where the instructions, 17 per value, take longer than the memory.
 //
 // The unit of work is a piece of sixteen consecutive values of a row: two
