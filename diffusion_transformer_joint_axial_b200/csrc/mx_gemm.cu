@@ -511,8 +511,8 @@ __device__ __forceinline__ void reuse_box() {
 // cache: 4096 x 4096 x 256 took 31 us with a residual, 21 without.)
 // SPLIT: one tile to a cluster of two pairs, each with half of K, for calls with few tiles.  When
 // both are done, the pairs swap halves of the tile's columns through shared
-// memory (fp32, [column][token]): pair i finishes what group i of its epilogue warps
-// holds, adding the other pair's sums to its own.
+// memory (fp32, [column][token]): pair i finishes columns 128 i .. 128 i + 127 (gated: hidden
+// features 64 i .. 64 i + 63), each of its warp groups half of them, adding the other pair's sums.
 template <bool GATED, bool SPLIT>
 __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -678,10 +678,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
       next_bias = t + pairs < tiles ? load_bias(t + pairs) : 0.f;
       const bool holds = !SPLIT && group != (int)buf;
       // plain: the columns of chunk i, the held ones first, and the next chunk that N reaches
-      auto chunk_col = [&](int i) { return 128 * group + (holds && group == 1 ? 32 * (i ^ 2) : 32 * i); };
-      const bool add = !GATED && p.residual != nullptr && row0 < p.M && !(SPLIT && group != part);
+      constexpr int kChunks = SPLIT ? 2 : 4;
+      auto chunk_col = [&](int i) {
+        return SPLIT ? 128 * part + 64 * group + 32 * i : 128 * group + (holds && group == 1 ? 32 * (i ^ 2) : 32 * i);
+      };
+      const bool add = !GATED && p.residual != nullptr && row0 < p.M;
       auto request = [&](int from, uint32_t box) {
-        for (int i = from; i < 4; ++i)
+        for (int i = from; i < kChunks; ++i)
           if (n0 + chunk_col(i) < p.N) {
             if (elect_one_sync()) {
               // the box's last store has been read: only the last one of all may not be
@@ -721,20 +724,18 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
       uint32_t others = 0;  // the other pair's sums of this thread's token and this group's first column
       if (SPLIT) {
         const uint32_t mine = smem_u32(S.x[0]) + ((warp & 3) * 32 + lane) * 4;
-        if (group != part) {
-          // this group's columns: plain 128; gated 64 gates, then 64 ups
+        // the other pair's columns, half by each group: plain 64 of 128; gated the gates, the ups
+        const int from = GATED ? 128 * group + 64 * (1 - part) : 128 * (1 - part) + 64 * group;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t v[32];
-            tmem_ld32(acc + (GATED ? (i < 2 ? 64 * group + 32 * i : 64 + 64 * group + 32 * i) : 128 * group + 32 * i), v);
-            tmem_wait_ld();
+        for (int i = 0; i < 2; ++i) {
+          uint32_t v[32];
+          tmem_ld32(acc + from + 32 * i, v);
+          tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              asm volatile("st.shared.b32 [%0], %1;" ::"r"(mine + (32 * i + e) * 512), "r"(v[e]) : "memory");
-          }
+          for (int e = 0; e < 32; ++e)
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(mine + (64 * group + 32 * i + e) * 512), "r"(v[e]) : "memory");
         }
         cluster_sync_all();
-        if (group != part) break;  // the other pair finishes these
         others = cluster_addr(mine, cluster_rank() ^ 2u);
       }
       if (GATED) {
@@ -742,16 +743,16 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
         reuse_box();
         uint32_t scales = 0;  // of the row's two blocks
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int c = 64 * group + 32 * i;
+        for (int i = 0; i < (SPLIT ? 1 : 2); ++i) {
+          const int c = SPLIT ? 64 * part + 32 * group : 64 * group + 32 * i;
           uint32_t v[32], u[32];
           // a held column is an up column in buffer 0, a gate column in buffer 1
           if (!(holds && buf == 1)) tmem_ld32(acc + c, v);
           if (!(holds && buf == 0)) tmem_ld32(acc + 128 + c, u);
           tmem_wait_ld();
           if (SPLIT) {
-            add_others(v, others + 32 * i * 512);
-            add_others(u, others + (64 + 32 * i) * 512);
+            add_others(v, others + 32 * group * 512);
+            add_others(u, others + (64 + 32 * group) * 512);
           }
           if (holds) {
 #pragma unroll
@@ -779,8 +780,15 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
             o.y = mx_cvt4(y[16 * g + 4] * inv, y[16 * g + 5] * inv, y[16 * g + 6] * inv, y[16 * g + 7] * inv);
             o.z = mx_cvt4(y[16 * g + 8] * inv, y[16 * g + 9] * inv, y[16 * g + 10] * inv, y[16 * g + 11] * inv);
             o.w = mx_cvt4(y[16 * g + 12] * inv, y[16 * g + 13] * inv, y[16 * g + 14] * inv, y[16 * g + 15] * inv);
-            *box_chunk(box, lane, 2 * i + g) = o;
+            if (!SPLIT)
+              *box_chunk(box, lane, 2 * i + g) = o;
+            else if (live)
+              reinterpret_cast<uint4*>(p.q + row * p.n_seg + (n0 >> 1) + c)[g] = o;
           }
+        }
+        if (SPLIT) {
+          if (live) p.scale[mx_scale_word(row, n, p.q_tile_cols) + 2 * part + group] = (uint8_t)scales;
+          continue;
         }
         if (row0 < p.M) {
           store_box(&p.tm_out[0], box, (n0 >> 1) + 64 * group, row0);
@@ -790,7 +798,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
           *reinterpret_cast<uint16_t*>(p.scale + mx_scale_word(row, n, p.q_tile_cols) + 2 * group) = (uint16_t)scales;
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kChunks; ++i) {
           // 32 columns to a box, the held ones first
           const int c = chunk_col(i);
           if (n0 + c >= p.N) continue;
@@ -803,7 +811,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
           uint32_t v[32];
           if (!(holds && i < 2)) tmem_ld32(acc + c, v);
           tmem_wait_ld();
-          if (SPLIT) add_others(v, others + 32 * i * 512);
+          if (SPLIT) add_others(v, others + (64 * group + 32 * i) * 512);
           if (holds && i < 2) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = held[i & 1][e];
@@ -1013,10 +1021,11 @@ static int64_t max64(int64_t a, int64_t b) { return a > b ? a : b; }
 // Which kernel for more than one tile of tokens: estimates, in ns, of a launch plus the rounds that the
 // tiles take over the SMs.  A round of the narrow kernel is its K steps and then its epilogue; of
 // the pairs' the longer of the two, as they overlap, except in the first.  The constants are fits to
-// measurements on a B200 (us, narrow / pairs / pairs with K split): 1024 x 4096 x 1024 8.6 / 9.4 / -,
-// 4096 x 12288 x 128 56 / 51 / -, 512 x 4096 x 4096 16.7 / 17.6 / 15, 512 x 4096 x 12288 39 / 38 / 27,
-// 1024 x 4096 x 12288 49 / 42 / -, 2048 x 4096 x 4096 38 / 31 / -, 4096 x 4096 x 256 with a residual 47 / 25 / -;
-// gated 1024 x 2048 x 128 8 / 5.7 / -, 333 x 2048 x 4096 20 / 16 / 13, 1000 x 4096 x 4096 44 / 30 / -.
+// measurements on a B200 (us, narrow / pairs / pairs with K split): 1024 x 4096 x 1024 8.0 / 9.5 / -,
+// 4096 x 12288 x 512 61 / 52 / -, 512 x 4096 x 4096 16 / 17.6 / 13.4, 512 x 4096 x 12288 39 / 38 / 25.6,
+// 1024 x 4096 x 12288 49 / 42 / -, 2048 x 4096 x 4096 38 / 31 / -, 4096 x 4096 x 256 with a residual 34 / 24 / -;
+// gated 1024 x 2048 x 128 6.6 / 5.7 / -, 333 x 2048 x 4096 20 / 16 / 12, 1000 x 4096 x 4096 44 / 30 / -.
+// Over 60 random shapes the chosen kernel was 1 % slower than the best of the three on average.
 static Way choose(const MxGemmArgs& a, int kt, int num_sms) {
   if (a.M <= 128) return Way::kNarrow;
   if (a.M > 128 * 65535ll) return Way::kWide;  // more token tiles than a grid's second axis takes
@@ -1027,14 +1036,15 @@ static Way choose(const MxGemmArgs& a, int kt, int num_sms) {
   const bool twos = !a.gated && ctas > num_sms;  // two CTAs to an SM
   const int64_t at_once = twos ? 2 * num_sms : num_sms, steps = (kt + c.split - 1) / c.split;
   const int64_t rounds = (ctas + at_once - 1) / at_once;
-  const int64_t res = a.residual == nullptr ? 0 : rounds > 1 ? 7000 : 3000;
+  const int64_t finish = (a.gated ? 4600 : rounds > 1 ? 3300 : 2400) + (act != 0 ? 1300 : 0) +
+                         (a.residual == nullptr ? 0 : rounds > 2 ? 4500 : 1500);
   const int64_t narrow = 1500 + (c.split == 1 ? 0 : split_cost(a.gated ? 2 : 1, c.bn)) +
-                         rounds * (3900 + act + res + steps * (a.gated ? 500 : twos ? 450 : 352));
+                         rounds * (finish + steps * (a.gated ? 500 : twos ? 450 : 352));
   const int64_t tiles = ((a.M + 255) / 256) * ((a.N + 255) / 256), pairs = num_sms / 2;
   const int64_t drain = (a.gated ? 2700 : 4400) + act + (a.residual != nullptr ? 1000 : 0);
   const int64_t wide = 2200 + drain + kt * 360 + ((tiles + pairs - 1) / pairs - 1) * max64(kt * 365 + 600, drain);
   // (of 37 clusters of four CTAs, one CTA to an SM, not all found room at once; 32 did)
-  const int64_t split = 4 * tiles <= num_sms - 20 && kt >= 8 ? 4500 + drain + (kt + 1) / 2 * 360 : INT64_MAX;
+  const int64_t split = 4 * tiles <= num_sms - 20 && kt >= 8 ? 3000 + drain + (kt + 1) / 2 * 360 : INT64_MAX;
   if (split < narrow && split < wide) return Way::kSplit;
   return wide < narrow ? Way::kWide : Way::kNarrow;
 }
