@@ -423,6 +423,28 @@ def test_two_streams_one_workspace_header(cuda_device):
         check_status(L["ws"])
 
 
+def test_every_kernel_at_once(cuda_device):
+    """Few and many tokens, whole and split over clusters, on four streams at a time: CTAs that hold tensor memory and
+    wait for others of their cluster share SMs with one another, and every call gives the same bits."""
+    rng = np.random.default_rng(23)
+    layers = [_layer(cuda_device, rng, M, 1024, 2048) for M in (1, 48, 400, 2300)]
+    want = []
+    for L in layers:
+        L["run"]()
+        want.append((L["out"].clone(), L["m"].q.view(torch.uint8).clone()))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(cuda_device) for _ in layers]
+    for i in range(60):
+        for k in range(len(layers)):
+            with torch.cuda.stream(streams[k]):
+                for _ in range(1 + (i + k) % 3):
+                    layers[k]["run"]()
+    torch.cuda.synchronize()
+    for L, (out, q) in zip(layers, want):
+        assert torch.equal(L["out"], out) and torch.equal(L["m"].q.view(torch.uint8), q)
+        check_status(L["ws"])
+
+
 def test_leading_dimensions_and_defaults(cuda_device):
     rng = np.random.default_rng(22)
     x = _act(rng, 6 * 50, 256).reshape(6, 50, 256).to(cuda_device)
