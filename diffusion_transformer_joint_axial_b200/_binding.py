@@ -549,17 +549,28 @@ def mx_empty(shape, device="cuda"):
                                 device=device).view(torch.float8_e8m0fnu))
 
 
+def _mx_scales(s, rows, K, device):
+    """Whether ``s`` is a scale tensor for [rows, K] on ``device``."""
+    return (isinstance(s, torch.Tensor) and s.shape == ((rows + 127) >> 7, (K + 127) >> 7, 32, 4, 4)
+            and s.dtype is _E8M0 and s.device == device and s.is_contiguous())
+
+
 def _need_mx(t, name, shape, rows, device):
     if not isinstance(t, MXTensor):
         raise QI21Error(QI21_ERR_INVALID_ARG, "%s must be an MXTensor" % name)
-    q, s = t
-    if (isinstance(q, torch.Tensor) and isinstance(s, torch.Tensor) and q.shape == shape
-            and s.shape == ((rows + 127) >> 7, (shape[-1] + 127) >> 7, 32, 4, 4) and q.dtype is _E4M3
-            and s.dtype is _E8M0 and q.device == device and s.device == device and q.is_contiguous()
-            and s.is_contiguous()):
-        return
-    _need(q, name + ".q", shape, _E4M3, device)
-    _need(s, name + ".scale", ((rows + 127) // 128, (shape[-1] + 127) // 128, 32, 4, 4), _E8M0, device)
+    _need(t.q, name + ".q", shape, _E4M3, device)
+    if not _mx_scales(t.scale, rows, shape[-1], device):
+        _need(t.scale, name + ".scale", ((rows + 127) // 128, (shape[-1] + 127) // 128, 32, 4, 4), _E8M0, device)
+
+
+def _need_operands(x, w, dev, shape, R, K, N):
+    """The MX operands of a product, x.q being a tensor of ``shape`` on ``dev``."""
+    xq, wq = x.q, w.q
+    if not (xq.dtype is _E4M3 and xq.is_contiguous() and _mx_scales(x.scale, R, K, dev)):
+        _need_mx(x, "x", shape, R, dev)
+    if not (wq.shape[1] == K and wq.dtype is _E4M3 and wq.device == dev and wq.is_contiguous()
+            and _mx_scales(w.scale, N, K, dev)):
+        _need_mx(w, "w", (N, K), N, dev)
 
 
 def _mx_operand(t, name):
@@ -580,7 +591,8 @@ def mx_quantize(x, out=None):
     attention output in front of a projection."""
     L_ = _mx_start(x, "x")
     dev, shape, K = x.device, x.shape, _mx_matrix(x, "x")
-    _need(x, "x", shape, torch.bfloat16, dev)
+    if x.dtype is not torch.bfloat16 or not x.is_contiguous():
+        _need(x, "x", shape, torch.bfloat16, dev)
     R = _rows(shape)
     if out is None:
         out = mx_empty(shape, dev)
@@ -595,7 +607,8 @@ def rmsnorm_mx(x, w, eps, delta=None, sum_out=None, out=None):
     delta), the norm is that of the stored h, and the result is ``(h, mx)``; without, just ``mx``."""
     L_ = _mx_start(x, "x")
     dev, shape, D = x.device, x.shape, _mx_matrix(x, "x")
-    _need(x, "x", shape, torch.bfloat16, dev)
+    if x.dtype is not torch.bfloat16 or not x.is_contiguous():
+        _need(x, "x", shape, torch.bfloat16, dev)
     _need(w, "w", (D,), torch.bfloat16, dev)
     R = _rows(shape)
     d_ptr = s_ptr = None
@@ -628,8 +641,7 @@ def linear_mx(x, w, bias=None, n_out=1, act="none", residual=None, alpha=1.0, ou
     if len(shape) < 1 or wq.dim() != 2:
         raise QI21Error(QI21_ERR_INVALID_ARG, "x must have rows and w two dimensions")
     K, N, R = shape[-1], wq.shape[0], _rows(shape)
-    _need_mx(x, "x", shape, R, dev)
-    _need_mx(w, "w", (N, K), N, dev)
+    _need_operands(x, w, dev, shape, R, K, N)
     if bias is not None:
         _need(bias, "bias", (N,), torch.bfloat16, dev)
     if act not in MX_ACTIVATIONS:
@@ -667,8 +679,7 @@ def linear_swiglu_mx(x, w_il, bias_il=None, out=None, workspace=None):
     if len(shape) < 1 or wq.dim() != 2:
         raise QI21Error(QI21_ERR_INVALID_ARG, "x must have rows and w two dimensions")
     K, N, R = shape[-1], wq.shape[0], _rows(shape)
-    _need_mx(x, "x", shape, R, dev)
-    _need_mx(w_il, "w", (N, K), N, dev)
+    _need_operands(x, w_il, dev, shape, R, K, N)
     if N % 256:
         raise QI21Error(QI21_ERR_INVALID_ARG, "the gate and up rows must come in blocks of 128 (N=%d)" % N)
     if bias_il is not None:
