@@ -66,8 +66,8 @@ __device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, u
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(sa), "r"(sb), "r"(accumulate)
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+      ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(sa), "r"(sb), "r"(accumulate)
       : "memory");
 }
 
@@ -96,8 +96,8 @@ __device__ __forceinline__ void mma_scaled_pair(uint32_t d, uint64_t a, uint64_t
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(sa), "r"(sb), "r"(accumulate)
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+      ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(sa), "r"(sb), "r"(accumulate)
       : "memory");
 }
 
@@ -107,9 +107,6 @@ __device__ __forceinline__ float silu(float y) { return __fdividef(y, 1.f + __ex
 // 0.5 y (1 + tanh(u)) = y / (1 + exp(-2u)),  u = sqrt(2/pi) (y + 0.044715 y^3)
 __device__ __forceinline__ float gelu_tanh(float y) {
   return __fdividef(y, 1.f + __expf(-1.5957691216057308f * fmaf(0.044715f * y * y, y, y)));
-}
-__device__ __forceinline__ float activate(float y, int act) {
-  return act == QI21_ACT_SILU ? silu(y) : act == QI21_ACT_GELU_TANH ? gelu_tanh(y) : y;
 }
 
 struct __align__(64) Params {
@@ -316,7 +313,8 @@ __global__ void __launch_bounds__(kNarrowThreads) mx_gemm_narrow(const __grid_co
       for (int e = 0; e < 16; ++e) {
         // a warp's 32 features are one scale block
         const uint32_t byte = mx_scale_byte(__reduce_max_sync(0xffffffffu, abs_bits(y[e])));
-        if (kAll || e < n) q[(uint64_t)((uint32_t)e) * (uint32_t)p.n_seg] = (uint8_t)mx_cvt2(y[e] * mx_inv_scale(byte), 0.f);
+        if (kAll || e < n)
+          q[(uint64_t)((uint32_t)e) * (uint32_t)p.n_seg] = (uint8_t)mx_cvt2(y[e] * mx_inv_scale(byte), 0.f);
         if (lane == e) mine = byte;
       }
       if (lane < (kAll ? 16 : n)) p.scale[mx_scale_word(row + lane, col >> 7, p.q_tile_cols) + quarter] = (uint8_t)mine;
@@ -326,7 +324,8 @@ __global__ void __launch_bounds__(kNarrowThreads) mx_gemm_narrow(const __grid_co
         // read and written by the same thread: the residual may be the output
         const __nv_bfloat16* r = p.residual + row * p.N + f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) res[e] = kAll || e < n ? __bfloat162float(r[(uint64_t)((uint32_t)e) * (uint32_t)p.N]) : 0.f;
+        for (int e = 0; e < 16; ++e)
+          res[e] = kAll || e < n ? __bfloat162float(r[(uint64_t)((uint32_t)e) * (uint32_t)p.N]) : 0.f;
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e) y[e] += bias;
@@ -381,7 +380,8 @@ __global__ void __launch_bounds__(kNarrowThreads) mx_gemm_narrow(const __grid_co
         tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + ((w * c.bn + t + e) * 128 + j) * 4), "r"(v[e]) : "memory");
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + ((w * c.bn + t + e) * 128 + j) * 4), "r"(v[e])
+                       : "memory");
       }
     }
     cluster_sync_all();
@@ -627,10 +627,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
             if (blocks >= 4) {
 #pragma unroll
               for (int b = 0; b < 4; ++b)
-                mma_scaled_pair(acc, xd + 2 * b, wd + 2 * b, idesc(256, 256) | idesc_block(b), sx, sw, kb > k_begin || b > 0);
+                mma_scaled_pair(acc, xd + 2 * b, wd + 2 * b, idesc(256, 256) | idesc_block(b), sx, sw,
+                                kb > k_begin || b > 0);
             } else {
               for (int b = 0; b < blocks; ++b)
-                mma_scaled_pair(acc, xd + 2 * b, wd + 2 * b, idesc(256, 256) | idesc_block(b), sx, sw, kb > k_begin || b > 0);
+                mma_scaled_pair(acc, xd + 2 * b, wd + 2 * b, idesc(256, 256) | idesc_block(b), sx, sw,
+                                kb > k_begin || b > 0);
             }
             mma_commit_pair(smem_u32(&S.empty[st]), first);
             if (kb == k_end - 1) mma_commit_pair(smem_u32(&S.acc_full[tc & 1u]), first);
@@ -733,7 +735,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(mine + (64 * group + 32 * i + e) * 512), "r"(v[e]) : "memory");
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(mine + (64 * group + 32 * i + e) * 512), "r"(v[e])
+                         : "memory");
         }
         cluster_sync_all();
         others = cluster_addr(mine, cluster_rank() ^ 2u);
@@ -830,7 +833,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
                                                    0x850));
             if (!ok) {
               const uint32_t next = slot + 1 == kBoxes ? 0 : slot + 1;
-              if (more) mbar_wait(smem_u32(&S.res_full[warp - 4][next]), next == 0 ? turn ^ 1u : turn, nullptr, nullptr, 0);
+              if (more)
+                mbar_wait(smem_u32(&S.res_full[warp - 4][next]), next == 0 ? turn ^ 1u : turn, nullptr, nullptr, 0);
               break;
             }
             coming = more;
@@ -854,8 +858,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
           }
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const uint4 o = make_uint4(pack_bf16x2(y[8 * g], y[8 * g + 1]), pack_bf16x2(y[8 * g + 2], y[8 * g + 3]),
-                                       pack_bf16x2(y[8 * g + 4], y[8 * g + 5]), pack_bf16x2(y[8 * g + 6], y[8 * g + 7]));
+            uint4 o;
+            o.x = pack_bf16x2(y[8 * g], y[8 * g + 1]);
+            o.y = pack_bf16x2(y[8 * g + 2], y[8 * g + 3]);
+            o.z = pack_bf16x2(y[8 * g + 4], y[8 * g + 5]);
+            o.w = pack_bf16x2(y[8 * g + 6], y[8 * g + 7]);
             if (boxed) {
               *box_chunk(box, lane, g) = o;
             } else if (live && n0 + c + 8 * g < p.N) {
@@ -892,8 +899,8 @@ static PFN_cuTensorMapEncodeTiled_v12000 mx_encode_fn() {
     cudaDriverEntryPointQueryResult q;
     const cudaError_t e =
         cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q);
-    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr)
-                                                                : nullptr;
+    const bool ok = e == cudaSuccess && q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr) : nullptr;
   }();
   return fn;
 }

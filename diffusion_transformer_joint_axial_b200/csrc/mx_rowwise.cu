@@ -128,7 +128,8 @@ __global__ void __launch_bounds__(256) rmsnorm_mx_kernel(int64_t M, int32_t D, i
   float2 ss = make_float2(0.f, 0.f);
   auto squares = [&](const float2 (&f)[8]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = make_float2(fmaf(f[e].x, f[e].x, ss.x), fmaf(f[e].y, f[e].y, ss.y));
+    for (int e = 0; e < 8; ++e)
+      ss = make_float2(fmaf(f[e].x, f[e].x, ss.x), fmaf(f[e].y, f[e].y, ss.y));
   };
   auto weigh = [&](float2 (&f)[8], const Piece& g) {
     float most = 0.f;
@@ -214,7 +215,8 @@ cudaError_t run_rmsnorm_mx(int64_t M, int32_t D, const void* x, const void* delt
   return launch_dependent(delta != nullptr ? rmsnorm_mx_kernel<TR, C, true> : rmsnorm_mx_kernel<TR, C, false>,
                           dim3((unsigned)((M + kRows - 1) / kRows)), 256, 0, 1, stream, M, D, (D + 127) / 128,
                           static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(delta),
-                          static_cast<const __nv_bfloat16*>(w), 1.f / static_cast<float>(D), eps, static_cast<__nv_bfloat16*>(sum),
+                          static_cast<const __nv_bfloat16*>(w), 1.f / static_cast<float>(D), eps,
+                          static_cast<__nv_bfloat16*>(sum),
                           static_cast<uint8_t*>(q), static_cast<uint8_t*>(scale));
 }
 
