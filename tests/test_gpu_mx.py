@@ -445,6 +445,50 @@ def test_every_kernel_at_once(cuda_device):
         check_status(L["ws"])
 
 
+def test_captured_across_streams(cuda_device):
+    """A capture that forks to a second stream and joins again, with copies and other kernels between the calls;
+    two graphs of it share one workspace."""
+    rng = np.random.default_rng(24)
+    dev, M, D = cuda_device, 300, 512
+    x, d = _act(rng, M, D).to(dev), _act(rng, M, D).to(dev)
+    nw = torch.ones(D, dtype=BF, device=dev)
+    w = qi.mx_quantize((_act(rng, 1024, D).float() * 0.05).to(BF).to(dev))
+    ws = qi.new_workspace(256, dev)
+    a, b, copy = qi.mx_empty((M, D), dev), qi.mx_empty((M, D), dev), torch.empty_like(x)
+    h, ya, yb = torch.empty_like(x), torch.empty(M, 1024, dtype=BF, device=dev), torch.empty(M, 1024, dtype=BF, device=dev)
+    other = torch.cuda.Stream(dev)
+
+    def run():
+        here = torch.cuda.current_stream()
+        copy.copy_(x)
+        qi.mx_quantize(copy, out=a)
+        other.wait_stream(here)
+        with torch.cuda.stream(other):
+            qi.rmsnorm_mx(copy, nw, 1e-6, delta=d, sum_out=h, out=b)
+            qi.linear_mx(b, w, out=[yb], workspace=ws)
+            h.mul_(2)
+        qi.linear_mx(a, w, act="silu", out=[ya], workspace=ws)
+        here.wait_stream(other)
+        qi.linear_mx(b, w, residual=ya, out=[ya], workspace=ws)
+
+    run()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (ya, yb, h)]
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run()
+        graphs.append(g)
+    for g in graphs * 3:
+        for t in (ya, yb, h):
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(t, v) for t, v in zip((ya, yb, h), want))
+    check_status(ws)
+
+
 def test_leading_dimensions_and_defaults(cuda_device):
     rng = np.random.default_rng(22)
     x = _act(rng, 6 * 50, 256).reshape(6, 50, 256).to(cuda_device)
