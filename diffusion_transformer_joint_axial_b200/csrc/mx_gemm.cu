@@ -386,6 +386,7 @@ __global__ void __launch_bounds__(kNarrowThreads) mx_gemm_narrow(const __grid_co
     }
     cluster_sync_all();
     const int share = (last + c.split - 1) / c.split, end = min(last, (rank + 1) * share);
+    bool reads = true;  // of the others' partials, until this warp's last ones are read
     for (int t = rank * share + t0; warp >= 2 && ok && t < end; t += 32) {
       const int n = min(16, end - t);
       float y[16] = {}, u[16] = {};
@@ -403,9 +404,14 @@ __global__ void __launch_bounds__(kNarrowThreads) mx_gemm_narrow(const __grid_co
           u[e] += pu[e];
         }
       }
+      if (t + 32 >= end) {
+        cluster_arrive();
+        reads = false;
+      }
       finish(t, n, y, u);
     }
-    cluster_sync_exit();  // nobody's partials go away while they are read
+    if (reads) cluster_arrive();
+    cluster_wait();  // nobody's partials go away while they are read
   }
   tc_fence_before();
   __syncthreads();
@@ -646,7 +652,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
       }
       __syncwarp();
     }
-    if (SPLIT) cluster_sync_all();  // the sums are there
+    if (SPLIT) {
+      cluster_sync_all();  // the sums are there
+      cluster_arrive();    // (these warps read none)
+    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ----------------------------------------------------------- epilogue
@@ -704,7 +713,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.acc_full[buf]), (tc >> 1) & 1u, abort_flag, p.status,
                                              0x840 | buf));
       if (!ok) {
-        if (SPLIT) cluster_sync_all();
+        if (SPLIT) {
+          cluster_sync_all();
+          cluster_arrive();
+        }
         break;
       }
       tc_fence_after();
@@ -756,6 +768,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
           if (SPLIT) {
             add_others(v, others + 32 * group * 512);
             add_others(u, others + (64 + 32 * group) * 512);
+            tc_fence_before();
+            cluster_arrive();
           }
           if (holds) {
 #pragma unroll
@@ -800,6 +814,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
         if (live)
           *reinterpret_cast<uint16_t*>(p.scale + mx_scale_word(row, n, p.q_tile_cols) + 2 * group) = (uint16_t)scales;
       } else {
+        bool reads = SPLIT;  // of the other pair's sums, until this warp's last ones are read
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
           // 32 columns to a box, the held ones first
@@ -814,7 +829,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
           uint32_t v[32];
           if (!(holds && i < 2)) tmem_ld32(acc + c, v);
           tmem_wait_ld();
-          if (SPLIT) add_others(v, others + (64 * group + 32 * i) * 512);
+          if (SPLIT) {
+            add_others(v, others + (64 * group + 32 * i) * 512);
+            if (i == kChunks - 1 || n0 + chunk_col(i + 1) >= p.N) {
+              tc_fence_before();
+              cluster_arrive();
+              reads = false;
+            }
+          }
           if (holds && i < 2) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = held[i & 1][e];
@@ -875,6 +897,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
             if (++slot == kBoxes) slot = 0, turn ^= 1u;
           }
         }
+        if (SPLIT && reads) {
+          tc_fence_before();
+          cluster_arrive();
+        }
       }
     }
     // (a request that a broken wait left behind lands before the CTA may exit)
@@ -885,7 +911,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
 
   tc_fence_before();
   __syncthreads();
-  cluster_sync_exit();
+  if (SPLIT)
+    cluster_wait();  // for the arrivals behind the reads of the other pair's sums
+  else
+    cluster_sync_exit();
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }

@@ -29,13 +29,20 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) 
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
   return a;
 }
-// Every thread of every CTA of the cluster; orders their shared memory.
-__device__ __forceinline__ void cluster_sync_all() {
+// Every thread of every CTA of the cluster, in two halves; orders their shared memory.  A thread that reads
+// other CTAs' shared memory arrives right behind its last read and waits before it leaves: the
+// arrival's release puts the reads in front of every CTA's exit, and the results' stores, which come
+// later, are not waited for.
+__device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The same without an order for memory: before leaving, so that no CTA's shared memory goes while others
-// still use it.  (Ordered, it would wait for the results' stores.)
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync_all() {
+  cluster_arrive();
+  cluster_wait();
+}
+// Before leaving, where no thread reads another CTA's shared memory itself: without an order for memory.
+// (Ordered, it would wait for the results' stores.)
 __device__ __forceinline__ void cluster_sync_exit() {
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
