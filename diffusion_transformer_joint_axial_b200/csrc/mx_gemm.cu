@@ -584,6 +584,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
             if (++st == kWideStages) st = 0, ph ^= 1u;
           }
         }
+        // The last products of every stage free it in both CTAs: their signals land here before this CTA may exit.
+        for (st = 0; ok && st < kWideStages; ++st)
+          if (it > st)
+            ok = mbar_wait(smem_u32(&S.empty[st]), ((it - 1 - st) / kWideStages) & 1u, abort_flag, p.status, 0x860 | st);
         if (!ok) {
           // Loads issued must land before the CTAs may exit.  Only the first CTA's
           // barriers see them; give the second one's the time that they need at most.
@@ -646,9 +650,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
             if (++slot == kSlots) slot = 0;
           }
         }
-        // every MMA issued completes before TMEM is released
         mma_commit_pair(smem_u32(&S.drain), first);
-        mbar_wait(smem_u32(&S.drain), 0, nullptr, nullptr, 0);
       }
       __syncwarp();
     }
@@ -723,7 +725,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
       const uint32_t acc = lane_base + kAccShift * buf;
       // The shared columns, the last 64 of buffer 0 (group 1's) and the first 64 of buffer 1
       // (group 0's), leave tensor memory first.  A group without any arrives too: it is
-      // done with the last tile.
+      // done with the last tile.  Nobody arrives where no tile follows: nothing would wait for
+      // the signal to land in the first CTA before it exits.
       uint32_t held[2][32];
       if (holds) {
         const uint32_t shared = buf == 0 ? 192 : 0;
@@ -733,7 +736,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
       }
       tc_fence_before();
       __syncwarp();
-      if (!SPLIT && lane == 0) mbar_arrive_cluster(free_bar);
+      if (!SPLIT && lane == 0 && t + pairs < tiles) mbar_arrive_cluster(free_bar);
       named_bar_sync(1 + group, 128);  // the biases are there (and the last tile's are no longer read)
       uint32_t others = 0;  // the other pair's sums of this thread's token and this group's first column
       if (SPLIT) {
@@ -911,6 +914,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
 
   tc_fence_before();
   __syncthreads();
+  if (warp == 1) {
+    // every MMA issued completes, and its signal has landed in both CTAs, before TMEM is released
+    if (elect_one_sync()) mbar_wait(smem_u32(&S.drain), 0, nullptr, p.status, 0x870);
+    __syncwarp();
+  }
   if (SPLIT)
     cluster_wait();  // for the arrivals behind the reads of the other pair's sums
   else

@@ -30,6 +30,22 @@ def _operand(gen, R, K, dev):
     (300, 4096, 4096, True),
     (385, 2560, 4096, True)])
 def test_nobody_leaves_while_its_sums_are_read(cuda_device, M, N, K, gated):
+    _same_bits_in_many_calls(cuda_device, M, N, K, gated)
+
+
+@pytest.mark.parametrize("M,N,K,gated", [
+    (300, 512, 160, True),     # pairs of one tile each, two stages of K
+    (900, 512, 96, True),
+    (300, 1024, 672, True),    # one stage more than there are slots for
+    (700, 1024, 416, True),
+    (2500, 6400, 160, True),   # several tiles a pair, one pair fewer tiles than another
+    (5000, 2056, 1056, False)])
+def test_pairs_leave_behind_every_signal(cuda_device, M, N, K, gated):
+    """Pairs whose last signals to the other CTA (a stage or an accumulator that is free) nothing waits for in turn."""
+    _same_bits_in_many_calls(cuda_device, M, N, K, gated)
+
+
+def _same_bits_in_many_calls(cuda_device, M, N, K, gated):
     """The same bits in every one of many calls, on two streams at a time, so that the shared memory of a CTA that
     left is written by another at once."""
     dev = cuda_device
