@@ -817,7 +817,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
         if (live)
           *reinterpret_cast<uint16_t*>(p.scale + mx_scale_word(row, n, p.q_tile_cols) + 2 * group) = (uint16_t)scales;
       } else {
-        bool reads = SPLIT;  // of the other pair's sums, until this warp's last ones are read
+        if (SPLIT) {
+          // both chunks' sums, own and the other pair's, before anything is stored
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            tmem_ld32(acc + chunk_col(i), held[i]);
+            tmem_wait_ld();
+            add_others(held[i], others + (64 * group + 32 * i) * 512);
+          }
+          tc_fence_before();
+          cluster_arrive();
+        }
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
           // 32 columns to a box, the held ones first
@@ -830,17 +840,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
           uint8_t* box = S.stage[warp - 4][slot];
           const bool more = add && request(i + 1, slot + 1 == kBoxes ? 0 : slot + 1);
           uint32_t v[32];
-          if (!(holds && i < 2)) tmem_ld32(acc + c, v);
+          if (!SPLIT && !(holds && i < 2)) tmem_ld32(acc + c, v);
           tmem_wait_ld();
-          if (SPLIT) {
-            add_others(v, others + (64 * group + 32 * i) * 512);
-            if (i == kChunks - 1 || n0 + chunk_col(i + 1) >= p.N) {
-              tc_fence_before();
-              cluster_arrive();
-              reads = false;
-            }
-          }
-          if (holds && i < 2) {
+          if (SPLIT || (holds && i < 2)) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = held[i & 1][e];
           }
@@ -899,10 +901,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
             store_box(&p.tm_out[seg], box, seg_col, row0);
             if (++slot == kBoxes) slot = 0, turn ^= 1u;
           }
-        }
-        if (SPLIT && reads) {
-          tc_fence_before();
-          cluster_arrive();
         }
       }
     }
