@@ -395,8 +395,11 @@ __global__ void __launch_bounds__(kNarrowThreads) mx_gemm_narrow(const __grid_co
         float py[16], pu[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          py[e] = e < n ? ld_cluster_f32(from + e * 512) : 0.f;
-          pu[e] = GATED && e < n ? ld_cluster_f32(from + (c.bn + e) * 512) : 0.f;
+          // (all sixteen are read, the last token's again where there are fewer: a test around each load
+          // made 64 x 4096 x 4096 take 12.0 us instead of 8.1)
+          const uint32_t at = from + min(e, n - 1) * 512;
+          py[e] = ld_cluster_f32(at);
+          pu[e] = GATED ? ld_cluster_f32(at + c.bn * 512) : 0.f;
         }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
