@@ -105,7 +105,9 @@ class DenoiseModel:
                 blk["w_gu"].copy_(qb.interleave_gate_up(blk["w_gu"]))
                 continue
             for k in ("w_qkv", "w_o", "w_gu", "w_down"):
-                w = theirs[k].to(self.device)
+                # through a bf16 copy: parameters of any float type, stride and device, as for the others
+                w = torch.empty(blk[k].q.shape, dtype=torch.bfloat16, device=self.device)
+                w.copy_(theirs[k], non_blocking=True)
                 qb.mx_quantize(qb.interleave_gate_up(w) if k == "w_gu" else w, out=blk[k])
 
     def _attend(self, i, A, n):
