@@ -91,15 +91,16 @@ class DenoiseModel:
     def load(self, params, x0, prefix_h):
         """Copies parameters (``workloads.denoise_model`` layout), the initial
         target latents [1, T, C] and the Prefix hidden states [1, P, D]."""
+        blocks = list(params["blocks"])  # gone through twice
         pairs = [(self.w_in, params["w_in"]), (self.b_in, params["b_in"]), (self.norm_out, params["norm_out"]),
                  (self.w_v, params["w_v"]), (self.b_v, params["b_v"]), (self.x, x0), (self.prefix_h, prefix_h)]
-        for mine, theirs in zip(self.blocks, params["blocks"]):
+        for mine, theirs in zip(self.blocks, blocks):
             pairs += [(mine[k], theirs[k]) for k in mine if isinstance(mine[k], torch.Tensor)]
         for dst, src in pairs:
             dst.copy_(src, non_blocking=True)
         # the feed-forward layer's [gate; up] weights go to the alternating
         # 128-row blocks of the fused projection + SwiGLU launch
-        for blk, theirs in zip(self.blocks, params["blocks"]):
+        for blk, theirs in zip(self.blocks, blocks):
             blk["b_gu"].copy_(qb.interleave_gate_up(blk["b_gu"]))
             if self.precision == "bf16":
                 blk["w_gu"].copy_(qb.interleave_gate_up(blk["w_gu"]))

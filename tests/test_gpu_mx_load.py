@@ -62,3 +62,10 @@ CHANGES = {
 def test_load_takes_types_and_strides(cuda_device, precision, change):
     """bf16 values in another type or layout load as the values themselves."""
     _assert_same_parameters(_loaded(cuda_device, precision, CHANGES[change]), _loaded(cuda_device, precision, lambda p: p))
+
+
+@pytest.mark.parametrize("precision", ["bf16", "mx"])
+def test_load_takes_blocks_from_an_iterator(cuda_device, precision):
+    """Parameters that a program produces block by block."""
+    _assert_same_parameters(_loaded(cuda_device, precision, lambda p: dict(p, blocks=iter(p["blocks"]))),
+                            _loaded(cuda_device, precision, lambda p: p))
