@@ -9,14 +9,14 @@ binding: it marshals torch tensors into that ABI and nothing else.
 from ._binding import (HEAD_DIM, LIB_PATH, MXTensor, QI21Error, Segment, alloc_cache, attn_cached, attn_full,
                        cached_workspace_size, full_workspace_size, interleave_gate_up, launch_count, linear,
                        linear_mx, linear_residual, linear_swiglu, linear_swiglu_mx,
-                       load_library, mx_empty, mx_quantize, new_workspace, rmsnorm, rmsnorm_mx, rope_positions,
-                       rope_table, rope_table_size, selftest_wait_timeout, swiglu, workspace_status)
+                       load_library, mx_empty, mx_plan, mx_quantize, new_workspace, rmsnorm, rmsnorm_mx,
+                       rope_positions, rope_table, rope_table_size, selftest_wait_timeout, swiglu, workspace_status)
 from . import denoise
 from .steploop import DenoiseLoop
 
 __all__ = ["DenoiseLoop", "HEAD_DIM", "LIB_PATH", "MXTensor", "QI21Error", "Segment", "alloc_cache",
            "attn_cached", "attn_full", "cached_workspace_size", "full_workspace_size", "interleave_gate_up",
            "launch_count", "linear", "linear_mx", "linear_residual", "linear_swiglu", "linear_swiglu_mx",
-           "load_library", "mx_empty", "mx_quantize", "new_workspace", "rmsnorm", "rmsnorm_mx",
+           "load_library", "mx_empty", "mx_plan", "mx_quantize", "new_workspace", "rmsnorm", "rmsnorm_mx",
            "rope_positions", "rope_table", "rope_table_size", "selftest_wait_timeout", "swiglu",
            "workspace_status"]

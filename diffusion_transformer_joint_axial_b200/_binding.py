@@ -39,7 +39,7 @@ EXPORTED = (
     "qi21_mx_scale_size", "qi21_mx_quantize", "qi21_rmsnorm_mx", "qi21_linear_mx", "qi21_linear_swiglu_mx",
     # status, errors, counters, timing and self-tests
     "qi21_workspace_status", "qi21_status_string", "qi21_last_error", "qi21_launch_count",
-    "qi21_selftest_wait_timeout",
+    "qi21_selftest_wait_timeout", "qi21_mx_plan",
 )
 
 
@@ -106,6 +106,8 @@ def load_library(path=LIB_PATH):
     L.qi21_linear_mx.restype = _i32
     L.qi21_linear_swiglu_mx.argtypes = [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
     L.qi21_linear_swiglu_mx.restype = _i32
+    L.qi21_mx_plan.argtypes = [_i64, _i64, _i64, _i32, _i32, _i32, _i32, ctypes.POINTER(_i32), ctypes.POINTER(_i32)]
+    L.qi21_mx_plan.restype = _i32
     L.qi21_workspace_status.argtypes = [_vp, _vp]
     L.qi21_selftest_wait_timeout.argtypes = [_vp, _i64, _vp]
     L.qi21_status_string.argtypes = [_i32]
@@ -696,6 +698,21 @@ def linear_swiglu_mx(x, w_il, bias_il=None, out=None, workspace=None):
              w_il.scale.data_ptr(), None if bias_il is None else bias_il.data_ptr(), out.q.data_ptr(),
              out.scale.data_ptr(), workspace.data_ptr(), workspace.nbytes)
     return out
+
+
+MX_KERNELS = ("few", "pairs", "pairs_split")
+
+
+def mx_plan(M, N, K, gated=False, act="none", residual=False, num_sms=0):
+    """(kernel, parts of K) that :func:`linear_mx`, or with ``gated`` :func:`linear_swiglu_mx` (N rows of W), runs for
+    these sizes on a GPU of ``num_sms`` SMs (0: the current device): "few" (128 features x up to 128 tokens a
+    CTA), "pairs" (256 x 256 a CTA pair) or "pairs_split".  Host only."""
+    if act not in MX_ACTIVATIONS:
+        raise QI21Error(QI21_ERR_INVALID_ARG, "unknown activation %r" % (act,))
+    kernel, parts = _i32(), _i32()
+    _check(load_library().qi21_mx_plan(M, N, K, int(gated), MX_ACTIVATIONS[act], int(residual), num_sms,
+                                       ctypes.byref(kernel), ctypes.byref(parts)))
+    return MX_KERNELS[kernel.value], parts.value
 
 
 def workspace_status(workspace, device=None):

@@ -730,6 +730,33 @@ qi21_status qi21_linear_swiglu_mx(int64_t M, int64_t N, int64_t K, const void* x
   return QI21_OK;
 }
 
+qi21_status qi21_mx_plan(int64_t M, int64_t N, int64_t K, int32_t gated, int32_t act, int32_t residual,
+                         int32_t num_sms, int32_t* kernel, int32_t* parts) {
+  QI21_TRY(check_mx_dims(M, K, "x"));
+  QI21_TRY(check_mx_dims(N, K, "w"));
+  if (M == 0 || N == 0) return fail(QI21_ERR_INVALID_ARG, "an empty product runs no kernel");
+  if (gated ? N % 256 != 0 || act != QI21_ACT_NONE || residual != 0 : N % 8 != 0)
+    return fail(QI21_ERR_INVALID_ARG,
+                "N must be a multiple of 8, or gated of 256 without activation and residual (got %lld)", (long long)N);
+  if (act < QI21_ACT_NONE || act > QI21_ACT_GELU_TANH)
+    return fail(QI21_ERR_INVALID_ARG, "unknown activation %d", act);
+  if (num_sms < 0 || num_sms == 1)
+    return fail(QI21_ERR_INVALID_ARG, "num_sms must be 0 or at least 2, a CTA pair (got %d)", num_sms);
+  if (kernel == nullptr || parts == nullptr) return fail(QI21_ERR_INVALID_ARG, "kernel and parts must not be NULL");
+  MxGemmArgs a;
+  memset(&a, 0, sizeof(a));
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.act = act;
+  a.gated = gated != 0;
+  a.residual = residual != 0 ? &a : nullptr;  // only whether there is one counts
+  const MxPlan plan = mx_gemm_plan(a, num_sms == 0 ? sm_count() : num_sms);
+  *kernel = plan.kernel;
+  *parts = plan.parts;
+  return QI21_OK;
+}
+
 // NULL names the built-in scratch of qi21_attn_cached_noalloc.
 static qi21_status status_target(void** workspace) {
   if (*workspace != nullptr) return QI21_OK;

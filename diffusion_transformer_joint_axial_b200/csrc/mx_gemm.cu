@@ -1060,7 +1060,6 @@ static cudaError_t launch_wide(mx::Params& p, const MxGemmArgs& a, cudaStream_t 
                           cluster, stream, p);
 }
 
-enum class Way { kNarrow, kWide, kSplit };
 static int64_t max64(int64_t a, int64_t b) { return a > b ? a : b; }
 
 // Which kernel for more than one tile of tokens: estimates, in ns, of a launch plus the rounds that the
@@ -1071,11 +1070,13 @@ static int64_t max64(int64_t a, int64_t b) { return a > b ? a : b; }
 // 1024 x 4096 x 12288 49 / 42 / -, 2048 x 4096 x 4096 38 / 31 / -, 4096 x 4096 x 256 with a residual 34 / 24 / -;
 // gated 1024 x 2048 x 128 6.6 / 5.7 / -, 333 x 2048 x 4096 20 / 16 / 12, 1000 x 4096 x 4096 44 / 30 / -.
 // Over 60 random shapes the chosen kernel was 1 % slower than the best of the three on average.
-static Way choose(const MxGemmArgs& a, int kt, int num_sms) {
-  if (a.M <= 128) return Way::kNarrow;
-  if (a.M > 128 * 65535ll) return Way::kWide;  // more token tiles than a grid's second axis takes
-  const int64_t act = a.act != QI21_ACT_NONE ? 2400 : 0;
+MxPlan mx_gemm_plan(const MxGemmArgs& a, int num_sms) {
+  const int kt = (int)((a.K + mx::BK - 1) / mx::BK);
   const mx::Narrow c = a.gated ? narrow_config<true>(a, kt, num_sms) : narrow_config<false>(a, kt, num_sms);
+  const MxPlan few{QI21_MX_FEW, c.split}, pairs_whole{QI21_MX_PAIRS, 1}, pairs_split{QI21_MX_PAIRS_SPLIT, 2};
+  if (a.M <= 128) return few;
+  if (a.M > 128 * 65535ll) return pairs_whole;  // more token tiles than a grid's second axis takes
+  const int64_t act = a.act != QI21_ACT_NONE ? 2400 : 0;
   const int64_t features = a.gated ? 256 : 128;
   const int64_t ctas = ((a.N + features - 1) / features) * ((a.M + 127) / 128) * c.split;
   const bool twos = !a.gated && ctas > num_sms;  // two CTAs to an SM
@@ -1090,8 +1091,8 @@ static Way choose(const MxGemmArgs& a, int kt, int num_sms) {
   const int64_t wide = 2200 + drain + kt * 360 + ((tiles + pairs - 1) / pairs - 1) * max64(kt * 365 + 600, drain);
   // (of 37 clusters of four CTAs, one CTA to an SM, not all found room at once; 32 did)
   const int64_t split = 4 * tiles <= num_sms - 20 && kt >= 8 ? 3000 + drain + (kt + 1) / 2 * 360 : INT64_MAX;
-  if (split < narrow && split < wide) return Way::kSplit;
-  return wide < narrow ? Way::kWide : Way::kNarrow;
+  if (split < narrow && split < wide) return pairs_split;
+  return wide < narrow ? pairs_whole : few;
 }
 
 cudaError_t launch_mx_gemm(const MxGemmArgs& a, cudaStream_t stream, int num_sms) {
@@ -1112,10 +1113,10 @@ cudaError_t launch_mx_gemm(const MxGemmArgs& a, cudaStream_t stream, int num_sms
   p.scale = static_cast<uint8_t*>(a.q_scale);
   p.q_tile_cols = p.n_seg / 128;
   p.status = a.status;
-  const Way way = choose(a, p.kt, num_sms);
-  if (way == Way::kWide)
+  const int32_t kernel = mx_gemm_plan(a, num_sms).kernel;
+  if (kernel == QI21_MX_PAIRS)
     return a.gated ? launch_wide<true, false>(p, a, stream, num_sms) : launch_wide<false, false>(p, a, stream, num_sms);
-  if (way == Way::kSplit)
+  if (kernel == QI21_MX_PAIRS_SPLIT)
     return a.gated ? launch_wide<true, true>(p, a, stream, num_sms) : launch_wide<false, true>(p, a, stream, num_sms);
   return a.gated ? launch_narrow<true>(p, a, stream, num_sms) : launch_narrow<false>(p, a, stream, num_sms);
 }

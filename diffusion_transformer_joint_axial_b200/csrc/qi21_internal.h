@@ -174,6 +174,12 @@ struct MxGemmArgs {
   uint32_t* status;         // workspace header status word
 };
 cudaError_t launch_mx_gemm(const MxGemmArgs& a, cudaStream_t stream, int num_sms);
+// Which kernel that runs for these sizes, activation and residual, and in how many parts of K.
+struct MxPlan {
+  int32_t kernel;  // qi21_mx_kernel
+  int32_t parts;
+};
+MxPlan mx_gemm_plan(const MxGemmArgs& a, int num_sms);
 
 // --------------------------------------------------------------- self test
 cudaError_t launch_wait_selftest(uint32_t* status, uint64_t limit_ns, cudaStream_t stream);

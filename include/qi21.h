@@ -448,6 +448,20 @@ qi21_status qi21_workspace_status(void* workspace, void* stream);
  * and exits normally; read it with qi21_workspace_status(). */
 qi21_status qi21_selftest_wait_timeout(void* workspace, int64_t limit_ns, void* stream);
 
+/* The kernels behind the MX products. */
+typedef enum {
+  QI21_MX_FEW = 0,        /* 128 features x up to 128 tokens to a CTA, K in `parts` over a cluster */
+  QI21_MX_PAIRS = 1,      /* 256 x 256 to a pair of CTAs */
+  QI21_MX_PAIRS_SPLIT = 2 /* the same, K in two parts over two pairs */
+} qi21_mx_kernel;
+
+/* Which of them qi21_linear_mx (gated = 0; with an activation, with a residual
+ * or not) or qi21_linear_swiglu_mx (gated = 1) runs for these sizes on a GPU of
+ * num_sms SMs (0: the current device; else at least 2), and into how many parts it cuts K.  Touches no
+ * GPU: a test can pin that its sizes reach the kernel that it is about. */
+qi21_status qi21_mx_plan(int64_t M, int64_t N, int64_t K, int32_t gated, int32_t act, int32_t residual,
+                         int32_t num_sms, int32_t* kernel, int32_t* parts);
+
 const char* qi21_status_string(qi21_status s);
 
 /* Message describing the last non-OK status returned to the calling thread. */

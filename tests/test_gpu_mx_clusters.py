@@ -1,7 +1,6 @@
 """The MX products whose CTAs read or signal one another (K split over a cluster, CTA pairs): calls in which some rows
 and features do not exist, so that some warps of a cluster have nothing to store and leave early."""
 
-import numpy as np
 import pytest
 import torch
 
@@ -30,6 +29,7 @@ def _operand(gen, R, K, dev):
     (300, 4096, 4096, True),
     (385, 2560, 4096, True)])
 def test_nobody_leaves_while_its_sums_are_read(cuda_device, M, N, K, gated):
+    assert qi.mx_plan(M, N, K, gated=gated) == (("few", 4) if M < 100 else ("pairs_split", 2))
     _same_bits_in_many_calls(cuda_device, M, N, K, gated)
 
 
@@ -42,6 +42,7 @@ def test_nobody_leaves_while_its_sums_are_read(cuda_device, M, N, K, gated):
     (5000, 2056, 1056, False)])
 def test_pairs_leave_behind_every_signal(cuda_device, M, N, K, gated):
     """Pairs whose last signals to the other CTA (a stage or an accumulator that is free) nothing waits for in turn."""
+    assert qi.mx_plan(M, N, K, gated=gated) == ("pairs", 1)
     _same_bits_in_many_calls(cuda_device, M, N, K, gated)
 
 
