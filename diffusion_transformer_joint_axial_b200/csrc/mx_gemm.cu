@@ -101,10 +101,12 @@ __device__ __forceinline__ void mma_scaled_pair(uint32_t d, uint64_t a, uint64_t
       : "memory");
 }
 
-// y / (1 + exp(-y)); the quotient is exact to a few units of 2^-24, far below
-// the rounding of the output.
+// y / (1 + exp(-y)).  The fast exponential's relative error grows with its argument, to about (2 + 1.2 |y|)
+// 2^-23, 1e-5 at |y| = 80: below the rounding of the output, 2^-8 (bf16) or 2^-4 (e4m3).  Where 1 + exp(-y)
+// exceeds 2^126 (y below -87.3) the quotient is 0 instead of a value below 2^-119.
 __device__ __forceinline__ float silu(float y) { return __fdividef(y, 1.f + __expf(-y)); }
-// 0.5 y (1 + tanh(u)) = y / (1 + exp(-2u)),  u = sqrt(2/pi) (y + 0.044715 y^3)
+// 0.5 y (1 + tanh(u)) = y / (1 + exp(-2u)),  u = sqrt(2/pi) (y + 0.044715 y^3); the same error with 2|u| in
+// the place of |y|, and 2^-22 |2u| for the rounding of u.
 __device__ __forceinline__ float gelu_tanh(float y) {
   return __fdividef(y, 1.f + __expf(-1.5957691216057308f * fmaf(0.044715f * y * y, y, y)));
 }

@@ -370,7 +370,7 @@ typedef enum {
   QI21_ACT_NONE = 0,
   QI21_ACT_SILU = 1,     /* y / (1 + exp(-y)) */
   QI21_ACT_GELU_TANH = 2 /* y / 2 (1 + tanh(sqrt(2 / pi) (y + 0.044715 y^3))) */
-} qi21_activation;
+} qi21_activation; /* both far below bf16's rounding, except that results below 2^-119 may become 0 */
 
 /*
  * qi21_linear_mx -- out = alpha * act(X W^T + b) (+ residual) with X [M, K] and
