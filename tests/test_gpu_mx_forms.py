@@ -152,3 +152,37 @@ def test_gated_rows_behind_the_last_stay(cuda_device, M, F, K, want):
     assert bool((q[M:] == 9).all()) and float((q[:M] == 9).double().mean()) < 0.1
     full = X.untile(scale.cpu().numpy(), groups * 128, F)
     assert (full[M:] == 0xAB).all() and (full[:M] != 0xAB).all()
+
+
+PADDED = [(1, 136, 96, False, ("few", 1)), (128, 264, 7456, False, ("few", 4)), (385, 1032, 4128, False, ("few", 2)),
+          (2601, 4104, 1184, False, ("pairs", 1)), (701, 2056, 3104, False, ("pairs_split", 2)),
+          (77, 512, 160, True, ("few", 1)), (905, 2304, 1056, True, ("pairs", 1)), (701, 2304, 3104, True, ("pairs_split", 2))]
+
+
+@pytest.mark.parametrize("M,N,K,gated,want", PADDED)
+def test_padding_of_scales_is_ignored(cuda_device, M, N, K, gated, want):
+    """Scale bytes of the rows and blocks that pad the last tiles may be anything, NaN among it."""
+    _plan(M, N, K, want, gated=gated)
+    rng = np.random.default_rng(M + N)
+    dev = cuda_device
+    x, _ = mx._mx_operand(rng, M, K, 1.0, dev)
+    w, _ = mx._mx_operand(rng, N, K, K ** -0.5, dev)
+
+    def run():
+        if gated:
+            t = qi.linear_swiglu_mx(x, w)
+            return t.q.view(torch.uint8)
+        return qi.linear_mx(x, w)[0]
+
+    want = run()
+    for t in (x, w):
+        s = t.scale.view(torch.uint8)
+        rows, cols = s.shape[0] * 128, s.shape[1] * 4
+        flat = s.permute(0, 3, 2, 1, 4).reshape(rows, cols)      # a copy: bytes by row and block
+        pad = torch.ones_like(flat, dtype=torch.bool)
+        pad[: t.q.shape[0], : K // 32] = False
+        assert bool(pad.any())
+        flat[pad] = 255
+        s.copy_(flat.view(s.shape[0], 4, 32, s.shape[1], 4).permute(0, 3, 2, 1, 4))
+        assert np.array_equal(X.untile(s.cpu().numpy(), *t.q.shape) == 255, np.zeros((t.q.shape[0], K // 32), dtype=bool))
+    assert torch.equal(run(), want)
