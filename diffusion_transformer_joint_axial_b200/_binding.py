@@ -585,7 +585,10 @@ def _mx_matrix(t, name):
     """The length of a row, where ``t`` has rows."""
     if t.dim() < 1:
         raise QI21Error(QI21_ERR_INVALID_ARG, "%s must have at least one dimension" % name)
-    return t.shape[-1]
+    K = t.shape[-1]
+    if K > 1 << 24:  # (the norm's entry point takes 32 bits of it)
+        raise QI21Error(QI21_ERR_INVALID_ARG, "the rows of %s are longer than 2^24 (%d)" % (name, K))
+    return K
 
 
 def mx_quantize(x, out=None):

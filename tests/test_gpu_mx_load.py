@@ -69,3 +69,11 @@ def test_load_takes_blocks_from_an_iterator(cuda_device, precision):
     """Parameters that a program produces block by block."""
     _assert_same_parameters(_loaded(cuda_device, precision, lambda p: dict(p, blocks=iter(p["blocks"]))),
                             _loaded(cuda_device, precision, lambda p: p))
+
+
+def test_rows_longer_than_an_int_are_refused(cuda_device):
+    """A row of 2^32 + 32 values, not of 32."""
+    x = torch.empty(1, 2 ** 32 + 32, dtype=BF, device=cuda_device)
+    for call in (lambda: qi.rmsnorm_mx(x, x[0], 1e-6), lambda: qi.mx_quantize(x)):
+        with pytest.raises(qi.QI21Error):
+            call()
