@@ -617,12 +617,31 @@ static qi21_status check_mx_dims(int64_t rows, int64_t K, const char* name) {
   return QI21_OK;
 }
 
+// A buffer of a call: what it is called, where it starts and its bytes.
+struct Span {
+  const char* name;
+  const void* at;
+  size_t bytes;
+};
+
+// A written buffer shares no byte with another one of the call; `whole`: it may be that one itself.
+static qi21_status check_apart(const Span& out, const Span& other, bool whole = false) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(out.at), b = reinterpret_cast<uintptr_t>(other.at);
+  if (other.at == nullptr || a >= b + other.bytes || b >= a + out.bytes || (whole && a == b)) return QI21_OK;
+  return fail(QI21_ERR_INVALID_ARG, "%s must not overlap %s", out.name, other.name);
+}
+
 qi21_status qi21_mx_quantize(int64_t M, int64_t K, const void* x, void* q, void* scale, void* stream) {
   QI21_TRY(check_mx_dims(M, K, "x"));
   if (M == 0) return QI21_OK;
   QI21_TRY(check_ptr(x, "x"));
   QI21_TRY(check_ptr(q, "q"));
   QI21_TRY(check_ptr(scale, "scale"));
+  const Span in{"x", x, (size_t)M * (size_t)K * 2}, values{"q", q, (size_t)M * (size_t)K},
+      scales{"scale", scale, qi21_mx_scale_size(M, K)};
+  QI21_TRY(check_apart(values, in));
+  QI21_TRY(check_apart(scales, in));
+  QI21_TRY(check_apart(values, scales));
   cudaError_t e = launch_mx_quantize(M, K, x, q, scale, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "MX quantise launch");
   return QI21_OK;
@@ -643,6 +662,16 @@ qi21_status qi21_rmsnorm_mx(int64_t M, int32_t D, const void* x, const void* del
   QI21_TRY(check_ptr(w, "w"));
   QI21_TRY(check_ptr(q, "q"));
   QI21_TRY(check_ptr(scale, "scale"));
+  const size_t bytes = (size_t)M * (size_t)D * 2;
+  const Span values{"q", q, bytes / 2}, scales{"scale", scale, qi21_mx_scale_size(M, D)}, total{"sum", sum, bytes};
+  const Span in[4] = {{"x", x, bytes}, {"delta", delta, bytes}, {"w", w, (size_t)D * 2}, total};
+  for (const Span& s : in) {
+    QI21_TRY(check_apart(values, s));
+    QI21_TRY(check_apart(scales, s));
+  }
+  QI21_TRY(check_apart(values, scales));
+  if (sum != nullptr)
+    for (int i = 0; i < 3; ++i) QI21_TRY(check_apart(total, in[i], i < 2));
   cudaError_t e = launch_rmsnorm_mx(M, D, x, delta, w, eps, sum, q, scale, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "MX RMSNorm launch");
   return QI21_OK;
@@ -680,6 +709,18 @@ static qi21_status mx_gemm_args(MxGemmArgs& a, bool* empty, int64_t M, int64_t N
   return QI21_OK;
 }
 
+// No result of an MX product overlaps what the product reads.
+static qi21_status check_mx_result(const MxGemmArgs& a, const Span& out) {
+  const size_t k = (size_t)a.K;
+  const Span in[5] = {{"x", a.x, (size_t)a.M * k},
+                      {"x_scale", a.x_scale, qi21_mx_scale_size(a.M, a.K)},
+                      {"w", a.w, (size_t)a.N * k},
+                      {"w_scale", a.w_scale, qi21_mx_scale_size(a.N, a.K)},
+                      {"bias", a.bias, (size_t)a.N * 2}};
+  for (const Span& s : in) QI21_TRY(check_apart(out, s));
+  return QI21_OK;
+}
+
 qi21_status qi21_linear_mx(int64_t M, int64_t N, int64_t K, const void* x, const void* x_scale, const void* w,
                            const void* w_scale, const void* bias, int32_t act, const void* residual, float alpha,
                            void* const* out, int32_t n_out, void* workspace, size_t workspace_bytes,
@@ -705,6 +746,12 @@ qi21_status qi21_linear_mx(int64_t M, int64_t N, int64_t K, const void* x, const
   a.alpha = alpha;
   for (int i = 0; i < n_out; ++i) a.out[i] = out[i];
   a.n_out = n_out;
+  const size_t bytes = (size_t)M * (size_t)(N / n_out) * 2;
+  for (int i = 0; i < n_out; ++i) {
+    QI21_TRY(check_mx_result(a, {"out[i]", out[i], bytes}));
+    QI21_TRY(check_apart({"out[i]", out[i], bytes}, {"the residual", residual, bytes}, true));
+    for (int j = 0; j < i; ++j) QI21_TRY(check_apart({"out[i]", out[i], bytes}, {"out[j]", out[j], bytes}));
+  }
   cudaError_t e = launch_mx_gemm(a, static_cast<cudaStream_t>(stream), sm_count());
   if (e != cudaSuccess) return cuda_fail(e, "MX linear launch");
   return QI21_OK;
@@ -722,6 +769,10 @@ qi21_status qi21_linear_swiglu_mx(int64_t M, int64_t N, int64_t K, const void* x
   if (empty) return QI21_OK;
   QI21_TRY(check_ptr(q, "q"));
   QI21_TRY(check_ptr(scale, "scale"));
+  const Span values{"q", q, (size_t)M * (size_t)(N / 2)}, scales{"scale", scale, qi21_mx_scale_size(M, N / 2)};
+  QI21_TRY(check_mx_result(a, values));
+  QI21_TRY(check_mx_result(a, scales));
+  QI21_TRY(check_apart(values, scales));
   a.gated = 1;
   a.q = q;
   a.q_scale = scale;

@@ -343,6 +343,9 @@ qi21_status qi21_swiglu(int64_t n, const void* g, const void* u, void* m, void* 
  * (it reads back as NaN, and so does every product with it).  They write the scales
  * of their M rows (and zero for the blocks past K in those rows' last tile),
  * never those of rows past M: readers ignore both.
+ *
+ * Each of the MX calls refuses a result that shares a byte with another buffer of
+ * the call, but for those that it may be itself as named below.
  */
 size_t qi21_mx_scale_size(int64_t rows, int64_t K);
 
@@ -361,7 +364,7 @@ qi21_status qi21_mx_quantize(int64_t M, int64_t K, const void* x, void* q, void*
  *   sum     device bf16 [M, D], written; given exactly when delta is.  It may be
  *           x or delta itself (each value is read before it is written).
  *   eps     finite, >= 0.
- *   q, scale  as for qi21_mx_quantize with K = D; they overlap no input.
+ *   q, scale  as for qi21_mx_quantize with K = D.
  */
 qi21_status qi21_rmsnorm_mx(int64_t M, int32_t D, const void* x, const void* delta, const void* w, float eps,
                             void* sum, void* q, void* scale, void* stream);
@@ -378,7 +381,7 @@ typedef enum {
  * (n_out segments as in qi21_linear), the down projection and the Euler step
  * (residual, alpha), and the two-layer MLPs of the text and time embeddings (act).
  * From one row (a time embedding) to every token of a request.
- *   x, x_scale  MX [M, K]; w, w_scale  MX [N, K].  Outputs overlap no input but the residual.
+ *   x, x_scale  MX [M, K]; w, w_scale  MX [N, K].
  *   bias        device bf16 [N] or NULL.
  *   act         qi21_activation.
  *   residual    device bf16 [M, N] or NULL (n_out = 1 with it); may be out[0].

@@ -77,3 +77,25 @@ def test_rows_longer_than_an_int_are_refused(cuda_device):
     for call in (lambda: qi.rmsnorm_mx(x, x[0], 1e-6), lambda: qi.mx_quantize(x)):
         with pytest.raises(qi.QI21Error):
             call()
+
+
+def test_results_in_place_of_operands(cuda_device):
+    """Through the binding: an 8-bit result in its own operand is refused, neighbours in one buffer are not."""
+    dev = cuda_device
+    gen = torch.Generator(device=dev).manual_seed(3)
+    a = qi.mx_quantize(torch.randn(300, 256, generator=gen, device=dev).to(BF))
+    w = qi.mx_quantize(torch.randn(512, 256, generator=gen, device=dev).to(BF))
+    want = qi.linear_swiglu_mx(a, w)
+    for out in (a, qi.MXTensor(want.q, a.scale), qi.MXTensor(a.q, want.scale)):
+        with pytest.raises(qi.QI21Error):
+            qi.linear_swiglu_mx(a, w, out=out)
+    y = torch.empty(2, 300, 256, dtype=BF, device=dev)
+    with pytest.raises(qi.QI21Error):
+        qi.linear_mx(a, w, n_out=2, out=[y[0], y[0]])
+    qi.linear_mx(a, w, n_out=2, out=[y[0], y[1]])
+    assert torch.equal(torch.cat([y[0], y[1]], 1), qi.linear_mx(a, w)[0])
+    both = torch.empty(2, 300, 256, dtype=torch.uint8, device=dev)
+    both[0] = a.q.view(torch.uint8)
+    x = qi.MXTensor(both[0].view(torch.float8_e4m3fn), a.scale)
+    got = qi.linear_swiglu_mx(x, w, out=qi.MXTensor(both[1].view(torch.float8_e4m3fn), want.scale.clone()))
+    assert torch.equal(got.q.view(torch.uint8), want.q.view(torch.uint8))
