@@ -141,9 +141,10 @@ struct __align__(64) Params {
 //   warp 0     TMA producer
 //   warp 1     TMEM owner and MMA issuer
 //   warps 2-9  epilogue: one feature per thread, every other sixteen tokens
-// Measured on a B200: 1 x 24576 x 4096 in 20.5 us (5.1 TB/s with launch and ramp), 16 x 4096 x 4096
-// in 7.5, 77 x 12288 x 4096 gated in 24 (4.3 TB/s), 1 x 4096 x 256 in 3.2.  Bound by HBM for few tokens, by
-// what an SM takes from L2 (64 bytes a cycle) for many.
+// Measured on a B200: 1 x 24576 x 4096 in 20.4 us (5.1 TB/s with launch and ramp), 16 x 4096 x 4096
+// in 7.9, 77 x 12288 x 4096 gated in 22.9 (4.5 TB/s: its 96 tiles leave 52 of 148 SMs idle, and two parts of K
+// would want more SMs than there are), 1 x 4096 x 256 in 3.1.  Bound by HBM for few tokens where there are
+// tiles enough, by what an SM takes from L2 (64 bytes a cycle) for many.
 //
 // Tensor memory and residency: a CTA waits in its allocation while others of the
 // SM hold the columns, and CTAs of a cluster wait for one another, so an SM must
@@ -437,11 +438,14 @@ __global__ void __launch_bounds__(kNarrowThreads) mx_gemm_narrow(const __grid_co
 // and [192, 448), and the scales of four K steps behind them.  The epilogue drains the
 // shared columns first and then lets the next tile's MMAs start, so only that
 // part of an epilogue is not hidden.
-// Measured on a B200: 4096 x 12288 x 4096 in 150 us, 2.75 PFLOP/s, the tensor pipe busy 73 % of
-// the cycles; gated 4096 x 24576 x 4096 in 288 us, 2.86 PFLOP/s, 80 %; 16384 rows of it in 1.25 ms
+// Measured on a B200: 4096 x 12288 x 4096 in 149 us, 2.77 PFLOP/s, the tensor pipe busy 75 % of
+// the cycles; gated 4096 x 24576 x 4096 in 283 us, 2.91 PFLOP/s, 82 %; 16384 rows of it in 1.11 ms, 1.26
 // under the power cap.  Bound by the tensor pipe and the shared memory that it and the TMA share: a
 // stage's MMAs take 512 cycles alone, about 600 beside the loads (the same with 4, 5 and 6 stages; with
-// stages of K = 256; without the scale copies).
+// stages of K = 256; without the scale copies).  With K below about 1300 (gated: 700) a tile's products are
+// done before the epilogue of the one in front, which then sets the pace: 1400 cycles a warp for 32 columns,
+// 880 of them arithmetic and packing (4096 x 12288 x 512 in 52 us, gated 4096 x 24576 x 256 in 62, at 18 % of
+// the tensor pipe).
 constexpr int kWideThreads = 384;
 constexpr int kWideStages = 5;
 constexpr int kGroup = 16;
@@ -592,7 +596,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) mx_gemm_wide(const __grid_con
         // The last products of every stage free it in both CTAs: their signals land here before this CTA may exit.
         for (st = 0; ok && st < kWideStages; ++st)
           if (it > st)
-            ok = mbar_wait(smem_u32(&S.empty[st]), ((it - 1 - st) / kWideStages) & 1u, abort_flag, p.status, 0x860 | st);
+            ok = mbar_wait(smem_u32(&S.empty[st]), ((it - 1 - st) / kWideStages) & 1u, abort_flag, p.status,
+                           0x860 | st);
         if (!ok) {
           // Loads issued must land before the CTAs may exit.  Only the first CTA's
           // barriers see them; give the second one's the time that they need at most.
@@ -1004,8 +1009,8 @@ static mx::Narrow narrow_config(const MxGemmArgs& a, int kt, int num_sms) {
   const int64_t tiles = ((a.N + NW * 128 - 1) / (NW * 128)) * ((a.M + c.bn - 1) / c.bn);
   // Parts of K: a step takes 310 ns; splitting costs barriers and remote reads, more with more
   // tokens, and pays only while SMs would idle (us in 1 / 2 / 4 / 8 parts: 16 x 4096 x 4096, 32 tiles,
-  // 12.7 / 9.2 / 8.0 / 9.8; 1 x 320 x 1568 6.4 / 5.8 / 5.6 / 6.9; 75 x 184 x 7456 22 / 15 / 10.5 / 11.3;
-  // 128 x 4096 x 1024 7.6 / 10.4).  Of 37 clusters of 4 CTAs, one to an SM, not all found room on
+  // 12.6 / 8.9 / 7.9 / 14.5; 1 x 320 x 1568 6.3 / 5.7 / 5.3 / 6.3; 75 x 184 x 7456 22 / 15 / 11.1 / 11.0;
+  // 128 x 4096 x 1024 5.8 / 6.9 / 7.7 / 13.9).  Of 37 clusters of 4 CTAs, one to an SM, not all found room on
   // the GPCs at once; 32 did.  One CTA per SM takes all of its shared memory for stages
   // (77 x 12288 x 4096 gated: 34 us with half, 25 with all); more tiles than SMs run in twos.
   c.split = 1;
@@ -1067,11 +1072,13 @@ static int64_t max64(int64_t a, int64_t b) { return a > b ? a : b; }
 // Which kernel for more than one tile of tokens: estimates, in ns, of a launch plus the rounds that the
 // tiles take over the SMs.  A round of the narrow kernel is its K steps and then its epilogue; of
 // the pairs' the longer of the two, as they overlap, except in the first.  The constants are fits to
-// measurements on a B200 (us, narrow / pairs / pairs with K split): 1024 x 4096 x 1024 8.0 / 9.5 / -,
-// 4096 x 12288 x 512 61 / 52 / -, 512 x 4096 x 4096 16 / 17.6 / 13.4, 512 x 4096 x 12288 39 / 38 / 25.6,
-// 1024 x 4096 x 12288 49 / 42 / -, 2048 x 4096 x 4096 38 / 31 / -, 4096 x 4096 x 256 with a residual 34 / 24 / -;
-// gated 1024 x 2048 x 128 6.6 / 5.7 / -, 333 x 2048 x 4096 20 / 16 / 12, 1000 x 4096 x 4096 44 / 30 / -.
-// Over 60 random shapes the chosen kernel was 1 % slower than the best of the three on average.
+// measurements on a B200 (us, narrow / pairs / pairs with K split): 1024 x 4096 x 1024 7.5 / 9.2 / -,
+// 4096 x 12288 x 512 60 / 52 / -, 512 x 4096 x 4096 14.9 / 16.1 / 13.7, 512 x 4096 x 12288 37 / 36 / 24.7,
+// 1024 x 4096 x 12288 49 / 43 / -, 2048 x 4096 x 4096 42 / 31 / -, 4096 x 4096 x 256 with a residual 36 / 25 / -;
+// gated 1024 x 2048 x 128 6.2 / 5.6 / -, 333 x 2048 x 4096 19 / 14 / 12.5, 1000 x 4096 x 4096 40 / 28 / -.
+// Over 60 random shapes the chosen kernel was 0.8 % slower than the best of the three on average, and the best for 54
+// of them (the narrow one for all of them: 16 % slower, the pairs without a split: 32 %); the worst by 32 %, 361 x
+// 6152 x 6112 with a residual, whose 147 CTAs of the narrow kernel take 570 ns a step from L2, not the estimate's 352.
 MxPlan mx_gemm_plan(const MxGemmArgs& a, int num_sms) {
   const int kt = (int)((a.K + mx::BK - 1) / mx::BK);
   const mx::Narrow c = a.gated ? narrow_config<true>(a, kt, num_sms) : narrow_config<false>(a, kt, num_sms);
