@@ -287,8 +287,9 @@ __global__ void __launch_bounds__(kNarrowThreads) mx_gemm_narrow(const __grid_co
   const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
   bool ok = true;
   if (warp >= 2) {
-    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&S.done), 0, abort_flag, p.status, 0x740));
-    ok = ok && !*abort_flag;
+    // (one vote: what follows under `ok` holds votes and barriers of whole warps)
+    ok = mbar_wait(smem_u32(&S.done), 0, abort_flag, p.status, 0x740) && !*abort_flag;
+    ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
   }
 
